@@ -101,6 +101,7 @@ typedef struct {
 #define MLA_ENTRY_OUT_PROJECT 2
 #define MLA_ENTRY_PREFILL 3
 #define MLA_ENTRY_DECODE 4
+#define MLA_ENTRY_TREE_DECODE 5
 
 /* Device workspace bytes that `entry` needs for these dims (has_topk = 1
  * if a topk_idx will be passed). 0 when nothing is needed or the dims are
@@ -257,6 +258,169 @@ int mla_attend_static(const mla_dims* dims, const void* q, const void* kv_latent
  * positive multiple of 128), MLA_ERR_ALIGN, MLA_ERR_CUDA. */
 int mla_quantize_act(const void* x, int rows, int cols, void* codes, float* scales, mla_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Serving over a paged cache: the calls around one decoding step in which
+ * every sequence brings one token or a tree of drafted tokens.
+ *
+ *   mla_rope               the queries' rotary part, by position
+ *   mla_cache_append       latent RMSNorm + key rotation, into cache rows
+ *   mla_tree_decode        attention over the pages, and W_o
+ *   mla_cache_compact      the accepted path's rows moved together
+ *   mla_cache_copy_pages   pages copied when a sequence forks
+ *
+ * The pages describe the rotary embedding, the latent norm and the decode
+ * step as steps of the model (MLA init: `kv_a_layernorm`, `_init_rope`,
+ * `freqs_cis`; decode: "scores the cached latent directly"); pages, trees
+ * and their upkeep have no counterpart there.
+ * ------------------------------------------------------------------------ */
+
+/* Rotary settings: made once per model with mla_rope_init, passed by pointer
+ * (host memory, read during the call only). */
+typedef struct {
+  uint64_t turns[32];  /* per pair: angle per position / 2 pi, in units of 2^-64 */
+  float magnitude;     /* multiplies every cosine and sine */
+  int layout;          /* MLA_ROPE_INTERLEAVED or MLA_ROPE_HALF */
+} mla_rope_table;
+
+#define MLA_ROPE_INTERLEAVED 0 /* pair i is elements 2i, 2i + 1 of the 64 */
+#define MLA_ROPE_HALF 1        /* pair i is elements i, 32 + i */
+
+#define MLA_ROPE_UNSCALED 0 /* f_i = base^(-2i/64) */
+#define MLA_ROPE_LINEAR 1   /* f_i / factor */
+#define MLA_ROPE_YARN 2     /* f_i / factor below, f_i above, a linear ramp between (see mla_rope_init) */
+
+/* Fills *table. Host only.
+ *   base    : > 1, finite (10000 for most models)
+ *   scaling : MLA_ROPE_UNSCALED (the arguments after it but `magnitude` are
+ *             ignored), MLA_ROPE_LINEAR (uses factor >= 1) or MLA_ROPE_YARN
+ *             (factor >= 1, original_len > 0, beta_fast >= beta_slow > 0):
+ *             with d(b) = 64 ln(original_len / (2 pi b)) / (2 ln base),
+ *             lo = max(floor(d(beta_fast)), 0), hi = min(ceil(d(beta_slow)), 63)
+ *             and r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1), pair i
+ *             turns by f_i (1 - r_i) + f_i / factor r_i per position.
+ *   magnitude: finite, multiplies cosines and sines (1 unless the model's
+ *             attention factor is applied here). YaRN models that scale the
+ *             scores instead pass that in the attention calls' `scale`.
+ * Errors: MLA_ERR_NULL, MLA_ERR_SHAPE (a value out of range),
+ * MLA_ERR_UNSUPPORTED (unknown layout or scaling). */
+int mla_rope_init(mla_rope_table* table, int layout, double base, int scaling, double factor, double original_len,
+                  double beta_fast, double beta_slow, float magnitude);
+
+/* Rotates 64 of each head's elements by the token's position:
+ *   (u, v) -> magnitude (u cos a - v sin a, v cos a + u sin a), a = position f_i
+ *   x, out     : bf16, element (row, head, e) at row * row_stride + head *
+ *                head_stride + e (strides in elements, multiples of 8)
+ *   width      : elements per head, a multiple of 8, at most 2048; elements
+ *                [offset, offset + 64) are rotated (offset a multiple of 8),
+ *                the others copied. For mla_prefill's q: 192 and 128; for a
+ *                rotary key: heads 1, width 64, offset 0.
+ *   positions  : int32 [rows], any value. The angle is exact to 2^-24 of half
+ *                a turn at every position.
+ *   inverse    : 1 rotates back (the sines negated): with the same magnitude
+ *                it is the transposed map, i.e. the gradient of the rotation.
+ * In place: out == x with equal strides; only the rotary elements are then
+ * touched. Any other overlap of x and out, or out rows that overlap one
+ * another, leave out undefined. fp32 arithmetic, one rounding. No workspace.
+ * Errors: MLA_ERR_NULL, MLA_ERR_SHAPE, MLA_ERR_UNSUPPORTED (layout),
+ * MLA_ERR_ALIGN, MLA_ERR_CUDA. rows * heads == 0 is a no-op. */
+int mla_rope(const mla_rope_table* table, const void* x, long long x_row_stride, long long x_head_stride, void* out,
+             long long out_row_stride, long long out_head_stride, int rows, int heads, int width, int offset,
+             const int32_t* positions, int inverse, mla_stream_t stream);
+
+/* A latent cache in pages: kv_cache bf16 [layers][num_pages][page_size][512],
+ * k_pe_cache bf16 [layers][num_pages][page_size][64]. Position t of sequence
+ * b is row t % page_size of page block_table[b][t / page_size] (the same page
+ * in every layer). A contiguous cache [B][T][512] with T a multiple of the
+ * page size is such a cache with the pages in order. */
+typedef struct {
+  int num_pages;
+  int page_size;    /* a power of two, 16 or more */
+  int table_width;  /* entries per sequence of block_table (0 where none is passed) */
+  int layers;       /* 1 for mla_tree_decode */
+} mla_pages;
+
+/* Fills cache rows: the latent RMSNorm and the key rotation of the model's
+ * kv_a projection, in one pass.
+ *   kv_a       : bf16, row r at r * kv_a_row_stride (elements, a multiple of
+ *                8, at least 576): 512 latent values, then 64 of the key
+ *   norm_weight: [512], fp32 if weight_is_f32, else bf16
+ *   eps        : finite, >= 0
+ *   positions  : int32 [rows] (for the rotation only)
+ *   slots      : int32 [rows]: the cache row (page * page_size + offset) of
+ *                each token; NULL: row r to cache row r. A token whose slot
+ *                lies outside [0, cache_rows) is not written (-1: padding).
+ *                A slot listed twice holds either token's values, 16-byte
+ *                piece by piece; list each once.
+ *   kv_cache   : bf16 [cache_rows][512]: norm_weight x / sqrt(mean x^2 + eps)
+ *   k_pe_cache : bf16 [cache_rows][64]: the rotated key
+ * Other rows stay as they are. fp32 arithmetic, one rounding. With slots NULL
+ * it makes mla_prefill's kv_latent and k_pe. Must not alias. Errors as for
+ * mla_rope. */
+int mla_cache_append(const mla_rope_table* table, const void* kv_a, long long kv_a_row_stride,
+                     const void* norm_weight, int weight_is_f32, float eps, const int32_t* positions,
+                     const int32_t* slots, int rows, void* kv_cache, void* k_pe_cache, long long cache_rows,
+                     mla_stream_t stream);
+
+/* Most nodes per sequence of mla_tree_decode. */
+#define MLA_MAX_TREE 64
+
+/* Attention of a tree of new tokens per sequence over its pages, and W_o:
+ * mla_decode for sequences of different lengths in a paged cache, with up to
+ * MLA_MAX_TREE queries each (N = 1: plain decode). The new tokens' rows must
+ * be in the cache already (mla_cache_append): node j of sequence b at
+ * position cache_len[b] + j, whatever its depth in the tree.
+ *   dims     : B sequences, T = N nodes per sequence (1 .. MLA_MAX_TREE), H,
+ *              wdtype; topk and path ignored, act must be MLA_ACT_BF16
+ *   q        : bf16 [B, N, H, 192], rotated
+ *   block_table: int32 [B, table_width]
+ *   cache_len: int32 [B], positions committed before the new ones (>= 0)
+ *   n_nodes  : int32 [B], new tokens of each sequence, clamped to [0, N];
+ *              NULL: N each
+ *   parents  : int32 [B, N]: the node each node hangs below. A node sees the
+ *              committed positions, itself and its ancestors. A value outside
+ *              [0, j) for node j: it hangs below the last committed position.
+ *              NULL: a chain (node j below node j - 1).
+ *   W_kvb, W_kvb_scale, W_o, W_o_scale, scale: as for mla_decode
+ *   out      : bf16 [B, N, 7168]; rows of nodes from n_nodes[b] on become 0
+ * Rows of the last page behind cache_len + n_nodes may hold anything, NaN
+ * included. Device errors (mla_device_status): 401 a needed block_table entry
+ * lies outside [0, num_pages): that sequence's out rows are undefined (nothing
+ * outside the caches is read); 402 cache_len < 0 or cache_len + n_nodes beyond
+ * the table: that sequence's out rows are 0.
+ * Workspace: mla_workspace_bytes(dims, MLA_ENTRY_TREE_DECODE, 0).
+ * Errors: as for mla_decode; MLA_ERR_SHAPE also for bad pages or N. */
+int mla_tree_decode(const mla_dims* dims, const mla_pages* pages, const void* q, const void* kv_cache,
+                    const void* k_pe_cache, const int32_t* block_table, const int32_t* cache_len,
+                    const int32_t* n_nodes, const int32_t* parents, const void* W_kvb, const float* W_kvb_scale,
+                    const void* W_o, const float* W_o_scale, float scale, void* out, void* workspace,
+                    size_t ws_bytes, mla_stream_t stream);
+
+/* Moves the rows of each sequence's accepted nodes together, in every layer:
+ * position cache_len[b] + accepted[b][i] to cache_len[b] + i, for
+ * i < n_accepted[b] (clamped to [0, width]). All of a sequence's rows are read
+ * before the first is written, so any order and any overlap is right.
+ *   accepted  : int32 [B, width], width 1 .. MLA_MAX_TREE
+ *   n_accepted: int32 [B]
+ * An entry whose source or destination lies outside the table or the cache
+ * moves nothing (device error 401). Sequences must not share the pages that
+ * are written. Stream-ordered, no workspace. Errors: MLA_ERR_NULL,
+ * MLA_ERR_SHAPE, MLA_ERR_ALIGN, MLA_ERR_CUDA. */
+int mla_cache_compact(const mla_pages* pages, void* kv_cache, void* k_pe_cache, const int32_t* block_table,
+                      const int32_t* cache_len, const int32_t* accepted, const int32_t* n_accepted, int B, int width,
+                      mla_stream_t stream);
+
+/* Copies page src[i] onto page dst[i], i < n, in every layer (a forked
+ * sequence's own copy of its last page). src and dst are HOST arrays, read
+ * during the call (a CUDA graph keeps the list it was captured with). A page
+ * may be the source of several pairs. MLA_ERR_SHAPE, with nothing copied, if
+ * an index is outside [0, num_pages), a page is the destination of two pairs,
+ * or the source of one pair and the destination of another; a pair with
+ * src == dst copies nothing but counts for these. table_width is ignored.
+ * Stream-ordered, no workspace. Errors: MLA_ERR_NULL, MLA_ERR_SHAPE,
+ * MLA_ERR_ALIGN, MLA_ERR_CUDA (also when the host is out of memory). */
+int mla_cache_copy_pages(const mla_pages* pages, void* kv_cache, void* k_pe_cache, const int32_t* src,
+                         const int32_t* dst, int n, mla_stream_t stream);
+
 /* Human-readable text of a status code (static storage). */
 const char* mla_status_str(int status);
 
@@ -265,7 +429,9 @@ const char* mla_status_str(int status);
  * kernel recorded: 1xx a pipeline wait timed out (101 TMA load, 102
  * tensor-core commit, 103 consumer release, 104 epilogue, 105 softmax
  * hand-off); 201 bad launch geometry; 301 an up-projected value v exceeded
- * the f16 range (|v| >= 65520) on the attention path (see mla_attend).
+ * the f16 range (|v| >= 65520) on the attention path (see mla_attend);
+ * 401 a page index outside the cache, 402 a length outside the block table
+ * (see mla_tree_decode, mla_cache_compact).
  * Returns MLA_ERR_CUDA if synchronisation fails, else MLA_OK. */
 int mla_device_status(mla_stream_t stream, int* device_error);
 
@@ -329,8 +495,9 @@ int mla_test_wo_split_plan(int tiles, int pairs, int num_kb, int* tail, int* spl
  * Classes: 0 topk prepass, 1 weight dequant, 2 W_kvb GEMM, 3 attention
  * (block-dense), 4 W_o GEMM, 5 per-row key lists (prefill and decode),
  * 6 absorb and un-absorb GEMMs, 7 attention (absorbed), 8 activation
- * quantization, 9 sums of the W_o GEMM's K-split last-wave tiles. Arrays
- * must hold MLA_PROFILE_CLASSES entries. */
+ * quantization, 9 sums of the W_o GEMM's K-split last-wave tiles.
+ * mla_tree_decode's launches count in 1, 4, 6 and 7; the rotation and cache
+ * calls (one kernel each) are not recorded. Arrays must hold MLA_PROFILE_CLASSES entries. */
 #define MLA_PROFILE_CLASSES 10
 int mla_profile_begin(void);
 int mla_profile_end(float* ms_total, int* launches);

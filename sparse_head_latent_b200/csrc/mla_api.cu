@@ -10,19 +10,23 @@
 #include <cstdint>
 #include <cstdio>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "../../include/mla.h"
 #include "attn.cuh"
 #include "attn_abs.cuh"
+#include "attn_tree.cuh"
 #include "dequant.cuh"
 #include "gemm2.cuh"
 #include "gemm_w8t.cuh"
 #include "gemm8.cuh"
 #include "gemm_m64.cuh"
+#include "pages.cuh"
 #include "prepass.cuh"
 #include "quant.cuh"
 #include "ptx.cuh"
+#include "rope.cuh"
 
 // Device error word: kernels record the first error code here.
 __device__ int g_mla_device_error;
@@ -293,6 +297,9 @@ constexpr int kStreamKCtas = 256;  // upper bound on the stream-K grid (the SM c
 constexpr int kSplitMinTileKb = 64;
 constexpr int kSplitMinKb = 8;
 constexpr int kSplitSlots = 74;
+// Up to this many rows the per-head GEMMs run on the few-row kernel (64- or
+// 128-row UMMA tiles, one CTA per item), beyond it on the CTA-pair GEMM.
+constexpr int kFewRows = 256;
 // Cost model for MLA_PATH_AUTO: a tile group goes absorbed when its middle
 // row's causal prefix exceeds this many times the selection size. Measured
 // on B200 at T = 32768, H = 128, top-k 2048: the block-dense kernel costs
@@ -393,7 +400,17 @@ WsLayout ws_layout(const mla_dims& d, int entry, bool has_topk) {
       w.wo_part = take((kStreamKCtas + tiles) * bm * 128 * 4);
     }
   }
-  const bool dec = entry == MLA_ENTRY_DECODE;
+  if (entry == MLA_ENTRY_TREE_DECODE && rows > 0) {
+    w.qabs = take(rows * H * kL * 2);
+    w.olat = take(rows * H * kL * 2);
+    w.attn = take(rows * H * kDv * 2);
+    if (rows <= kFewRows) {
+      const int bm = rows <= 64 ? 64 : 128;
+      const size_t tiles = (rows + bm - 1) / bm * (kD / 128);
+      w.wo_part = take((kStreamKCtas + tiles) * bm * 128 * 4);
+    }
+  }
+  const bool dec = entry == MLA_ENTRY_DECODE || entry == MLA_ENTRY_TREE_DECODE;
   const bool act8 = d.act == MLA_ACT_E4M3_DYNAMIC;
   if (act8) {
     if (attend || entry == MLA_ENTRY_KV_UPPROJECT) {
@@ -784,10 +801,6 @@ int launch_decode_lists(const mla_dims& d, const int32_t* topk, int kpad, int32_
   });
 }
 
-// Up to this many rows the per-head GEMMs run on the few-row kernel (64- or
-// 128-row UMMA tiles, one CTA per item), beyond it on the CTA-pair GEMM.
-constexpr int kFewRows = 256;
-
 // q_abs[r, h, :] = q[r, h, 0:128] . W_kvb[h*256 + (0..127), :] for `rows`
 // consecutive rows: one GEMM per head (M = rows, N = 512, K = 128).
 int launch_gemm_absorb(const DeviceState* ds, int H, int rows, const void* q_rows, const void* wk, void* qabs,
@@ -1036,6 +1049,86 @@ int run_decode(const DeviceState* ds, const mla_dims& d, const WsLayout& lay, vo
   return launch_gemm_wo(ds, d.B, d.H, attn, wo, out, st);
 }
 
+// ------------------------------------------------------------------ paged serving
+
+constexpr int64_t kMaxCacheRows = int64_t(1) << 30;  // rows of one layer's cache, positions of one table row
+constexpr int kMaxLayers = 65535;                    // a grid dimension
+
+int check_pages(const mla_pages* pg, bool table) {
+  if (pg == nullptr) return MLA_ERR_NULL;
+  if (pg->num_pages < 0 || pg->page_size < 16 || (pg->page_size & (pg->page_size - 1)) != 0) return MLA_ERR_SHAPE;
+  if (static_cast<int64_t>(pg->num_pages) * pg->page_size > kMaxCacheRows) return MLA_ERR_SHAPE;
+  if (pg->layers < 1 || pg->layers > kMaxLayers) return MLA_ERR_SHAPE;
+  if (table && (pg->table_width < 1 || static_cast<int64_t>(pg->table_width) * pg->page_size > kMaxCacheRows))
+    return MLA_ERR_SHAPE;
+  return MLA_OK;
+}
+
+int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
+mla::RopeTable rope_table(const mla_rope_table& t) {
+  mla::RopeTable r;
+  for (int i = 0; i < mla::kRopePairs; ++i) r.turns[i] = t.turns[i];
+  r.magnitude = t.magnitude;
+  r.layout = t.layout;
+  return r;
+}
+
+// One decoding step of B trees of N nodes.
+int run_tree_decode(const DeviceState* ds, const mla_dims& d, const mla_pages& pg, const WsLayout& lay, void* ws,
+                    const void* q, const void* kv, const void* pe, const int32_t* table, const int32_t* cache_len,
+                    const int32_t* n_nodes, const int32_t* parents, const void* W_kvb, const float* W_kvb_scale,
+                    const void* W_o, const float* W_o_scale, float scale, void* out, cudaStream_t st) {
+  const int rows = d.B * d.T;
+  const void* wk = W_kvb;
+  int rc = MLA_OK;
+  if (d.wdtype == MLA_W_E4M3_BLOCK128) {
+    void* dq = ws_at(ws, lay.wkvb);
+    if ((rc = launch_dequant(ds, W_kvb, W_kvb_scale, dq, d.H * (kDn + kDv), kL, st)) != MLA_OK) return rc;
+    wk = dq;
+  }
+  void* qabs = ws_at(ws, lay.qabs);
+  void* olat = ws_at(ws, lay.olat);
+  void* attn = ws_at(ws, lay.attn);
+  if ((rc = launch_gemm_absorb(ds, d.H, rows, q, wk, qabs, st)) != MLA_OK) return rc;
+  mla::TreeParams p;
+  p.B = d.B;
+  p.N = d.T;
+  p.H = d.H;
+  p.num_pages = pg.num_pages;
+  p.page_shift = log2_of(pg.page_size);
+  p.table_width = pg.table_width;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.table = table;
+  p.cache_len = cache_len;
+  p.n_nodes = n_nodes;
+  p.parents = parents;
+  p.qabs = static_cast<const __nv_bfloat16*>(qabs);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.kv = static_cast<const __nv_bfloat16*>(kv);
+  p.pe = static_cast<const __nv_bfloat16*>(pe);
+  p.olat = static_cast<__nv_bfloat16*>(olat);
+  p.err = ds->err;
+  rc = timed_launch(7, st, [&] {
+    mla::tree_attn_kernel<<<rows * ((d.H + mla::kTreeWarps - 1) / mla::kTreeWarps), 32 * mla::kTreeWarps, 0, st>>>(p);
+  });
+  if (rc != MLA_OK) return rc;
+  if ((rc = launch_gemm_unabsorb(ds, d.H, rows, olat, wk, attn, st)) != MLA_OK) return rc;
+  const void* wo = W_o;
+  if (d.wdtype == MLA_W_E4M3_BLOCK128) {
+    void* dq = ws_at(ws, lay.wo);
+    if ((rc = launch_dequant(ds, W_o, W_o_scale, dq, d.H * kDv, kD, st)) != MLA_OK) return rc;
+    wo = dq;
+  }
+  if (lay.wo_part != kNone)
+    return launch_gemm_wo_m64(ds, rows, d.H, attn, wo, reinterpret_cast<float*>(ws_at(ws, lay.wo_part)), out, st);
+  return launch_gemm_wo(ds, rows, d.H, attn, wo, out, st);
+}
+
 bool fp8_scales_ok(const mla_dims* d, const float* s) { return d->wdtype != MLA_W_E4M3_BLOCK128 || s != nullptr; }
 
 }  // namespace
@@ -1043,8 +1136,9 @@ bool fp8_scales_ok(const mla_dims* d, const float* s) { return d->wdtype != MLA_
 extern "C" {
 
 size_t mla_workspace_bytes(const mla_dims* dims, int entry, int has_topk) {
-  if (check_dims(dims) != MLA_OK || entry < MLA_ENTRY_KV_UPPROJECT || entry > MLA_ENTRY_DECODE) return 0;
-  if (entry == MLA_ENTRY_DECODE && dims->act != MLA_ACT_BF16) return 0;
+  if (check_dims(dims) != MLA_OK || entry < MLA_ENTRY_KV_UPPROJECT || entry > MLA_ENTRY_TREE_DECODE) return 0;
+  if ((entry == MLA_ENTRY_DECODE || entry == MLA_ENTRY_TREE_DECODE) && dims->act != MLA_ACT_BF16) return 0;
+  if (entry == MLA_ENTRY_TREE_DECODE && dims->T > MLA_MAX_TREE) return 0;
   return ws_layout(*dims, entry, has_topk != 0).total;
 }
 
@@ -1171,6 +1265,259 @@ int mla_quantize_act(const void* x, int rows, int cols, void* codes, float* scal
   const int rc = device_state(&ds);
   if (rc != MLA_OK) return rc;
   return launch_quant(x, rows, cols, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mla_rope_init(mla_rope_table* table, int layout, double base, int scaling, double factor, double original_len,
+                  double beta_fast, double beta_slow, float magnitude) {
+  if (table == nullptr) return MLA_ERR_NULL;
+  if (layout != MLA_ROPE_INTERLEAVED && layout != MLA_ROPE_HALF) return MLA_ERR_UNSUPPORTED;
+  if (scaling != MLA_ROPE_UNSCALED && scaling != MLA_ROPE_LINEAR && scaling != MLA_ROPE_YARN)
+    return MLA_ERR_UNSUPPORTED;
+  if (!(base > 1.0) || !std::isfinite(base) || !std::isfinite(magnitude)) return MLA_ERR_SHAPE;
+  if (scaling != MLA_ROPE_UNSCALED && (!(factor >= 1.0) || !std::isfinite(factor))) return MLA_ERR_SHAPE;
+  const double pi = 3.14159265358979323846;
+  double lo = 0.0, hi = 0.0;
+  if (scaling == MLA_ROPE_YARN) {
+    if (!(original_len > 0.0) || !std::isfinite(original_len) || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) ||
+        !std::isfinite(beta_fast))
+      return MLA_ERR_SHAPE;
+    const double per = mla::kRopeDim / (2.0 * std::log(base));
+    lo = std::fmax(std::floor(per * std::log(original_len / (2.0 * pi * beta_fast))), 0.0);
+    hi = std::fmin(std::ceil(per * std::log(original_len / (2.0 * pi * beta_slow))), mla::kRopeDim - 1.0);
+  }
+  for (int i = 0; i < mla::kRopePairs; ++i) {
+    double f = std::pow(base, -2.0 * i / mla::kRopeDim);
+    if (scaling == MLA_ROPE_LINEAR) f /= factor;
+    if (scaling == MLA_ROPE_YARN) {
+      const double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3), 0.0), 1.0);
+      f = f * (1.0 - r) + f / factor * r;
+    }
+    // f <= 1 radian per position, so the fraction of a turn fits (2^64 / 2 pi < 2^62)
+    table->turns[i] = static_cast<uint64_t>(static_cast<long double>(f) / (2.0L * 3.14159265358979323846264338328L) *
+                                                18446744073709551616.0L +
+                                            0.5L);
+  }
+  table->magnitude = magnitude;
+  table->layout = layout;
+  return MLA_OK;
+}
+
+int mla_rope(const mla_rope_table* table, const void* x, long long x_row_stride, long long x_head_stride, void* out,
+             long long out_row_stride, long long out_head_stride, int rows, int heads, int width, int offset,
+             const int32_t* positions, int inverse, mla_stream_t stream) {
+  if (table == nullptr) return MLA_ERR_NULL;
+  if (table->layout != MLA_ROPE_INTERLEAVED && table->layout != MLA_ROPE_HALF) return MLA_ERR_UNSUPPORTED;
+  if (rows < 0 || heads < 0 || width < mla::kRopeDim || width > 2048 || width % 8 != 0) return MLA_ERR_SHAPE;
+  if (offset < 0 || offset % 8 != 0 || offset + mla::kRopeDim > width) return MLA_ERR_SHAPE;
+  if ((inverse != 0 && inverse != 1) || x_row_stride % 8 != 0 || x_head_stride % 8 != 0 || out_row_stride % 8 != 0 ||
+      out_head_stride % 8 != 0)
+    return MLA_ERR_SHAPE;
+  if (rows == 0 || heads == 0) return MLA_OK;
+  if (!x || !out || !positions) return MLA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(out) || (reinterpret_cast<uintptr_t>(positions) & 3u)) return MLA_ERR_ALIGN;
+  DeviceState* ds = nullptr;
+  const int rc = device_state(&ds);
+  if (rc != MLA_OK) return rc;
+  mla::RopeParams p;
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.x_row = x_row_stride;
+  p.x_head = x_head_stride;
+  p.o_row = out_row_stride;
+  p.o_head = out_head_stride;
+  p.rows = rows;
+  p.heads = heads;
+  const bool in_place = x == out && x_row_stride == out_row_stride && x_head_stride == out_head_stride;
+  p.rope_chunk = offset / 8;
+  p.first = in_place ? p.rope_chunk : 0;
+  p.chunks = in_place ? mla::kRopeDim / 8 : width / 8;
+  p.inverse = inverse != 0;
+  p.positions = positions;
+  // Blocks: a row's heads split until about eight blocks per SM exist, or
+  // several rows to a block when one row's heads do not fill it.
+  const int groups = mla::kRopeThreads / p.chunks;
+  p.rows_per_block = groups / heads;
+  int64_t grid;
+  if (p.rows_per_block > 1) {
+    p.head_blocks = 1;
+    p.heads_per_block = heads;
+    grid = (static_cast<int64_t>(rows) + p.rows_per_block - 1) / p.rows_per_block;
+  } else {
+    p.rows_per_block = 1;
+    const int most = (heads + groups - 1) / groups;
+    int64_t split = (int64_t(8) * ds->sms + rows - 1) / rows;
+    if (split > most) split = most;
+    p.heads_per_block = (most + static_cast<int>(split) - 1) / static_cast<int>(split) * groups;
+    p.head_blocks = (heads + p.heads_per_block - 1) / p.heads_per_block;
+    grid = static_cast<int64_t>(rows) * p.head_blocks;
+  }
+  if (grid > 0x7fffffff) return MLA_ERR_SHAPE;
+  const mla::RopeTable tab = rope_table(*table);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (tab.layout == MLA_ROPE_HALF)
+    mla::rope_kernel<true><<<static_cast<unsigned>(grid), mla::kRopeThreads, 0, st>>>(tab, p);
+  else
+    mla::rope_kernel<false><<<static_cast<unsigned>(grid), mla::kRopeThreads, 0, st>>>(tab, p);
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_cache_append(const mla_rope_table* table, const void* kv_a, long long kv_a_row_stride,
+                     const void* norm_weight, int weight_is_f32, float eps, const int32_t* positions,
+                     const int32_t* slots, int rows, void* kv_cache, void* k_pe_cache, long long cache_rows,
+                     mla_stream_t stream) {
+  if (table == nullptr) return MLA_ERR_NULL;
+  if (table->layout != MLA_ROPE_INTERLEAVED && table->layout != MLA_ROPE_HALF) return MLA_ERR_UNSUPPORTED;
+  if (rows < 0 || cache_rows < 0 || kv_a_row_stride % 8 != 0 || kv_a_row_stride < kL + kDr) return MLA_ERR_SHAPE;
+  if (!(eps >= 0.f) || !std::isfinite(eps) || (weight_is_f32 != 0 && weight_is_f32 != 1)) return MLA_ERR_SHAPE;
+  if (rows == 0 || cache_rows == 0) return MLA_OK;
+  if (!kv_a || !norm_weight || !positions || !kv_cache || !k_pe_cache) return MLA_ERR_NULL;
+  if (!aligned16(kv_a) || !aligned16(norm_weight) || !aligned16(kv_cache) || !aligned16(k_pe_cache) ||
+      ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots)) & 3u))
+    return MLA_ERR_ALIGN;
+  DeviceState* ds = nullptr;
+  const int rc = device_state(&ds);
+  if (rc != MLA_OK) return rc;
+  mla::AppendParams p;
+  p.kv_a = static_cast<const __nv_bfloat16*>(kv_a);
+  p.kv_row = kv_a_row_stride;
+  p.weight = norm_weight;
+  p.weight_f32 = weight_is_f32 != 0;
+  p.eps = eps;
+  p.positions = positions;
+  p.slots = slots;
+  p.kv = static_cast<__nv_bfloat16*>(kv_cache);
+  p.pe = static_cast<__nv_bfloat16*>(k_pe_cache);
+  p.rows = rows;
+  p.cache_rows = cache_rows;
+  const mla::RopeTable tab = rope_table(*table);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = (static_cast<unsigned>(rows) + 3) / 4;
+  if (tab.layout == MLA_ROPE_HALF)
+    mla::cache_append_kernel<true><<<grid, 128, 0, st>>>(tab, p);
+  else
+    mla::cache_append_kernel<false><<<grid, 128, 0, st>>>(tab, p);
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_tree_decode(const mla_dims* dims, const mla_pages* pages, const void* q, const void* kv_cache,
+                    const void* k_pe_cache, const int32_t* block_table, const int32_t* cache_len,
+                    const int32_t* n_nodes, const int32_t* parents, const void* W_kvb, const float* W_kvb_scale,
+                    const void* W_o, const float* W_o_scale, float scale, void* out, void* workspace,
+                    size_t ws_bytes, mla_stream_t stream) {
+  DeviceState* ds = nullptr;
+  WsLayout lay;
+  int rc = check_dims(dims);
+  if (rc != MLA_OK) return rc;
+  if (dims->T > MLA_MAX_TREE) return MLA_ERR_SHAPE;
+  if (static_cast<int64_t>(dims->B) * dims->T == 0) return MLA_OK;
+  if ((rc = check_pages(pages, true)) != MLA_OK) return rc;
+  if (pages->layers != 1 || pages->num_pages < 1) return MLA_ERR_SHAPE;
+  if (!q || !kv_cache || !k_pe_cache || !block_table || !cache_len || !W_kvb || !W_o || !out ||
+      !fp8_scales_ok(dims, W_kvb_scale) || !fp8_scales_ok(dims, W_o_scale))
+    return MLA_ERR_NULL;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return MLA_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(k_pe_cache) || !aligned16(W_kvb) || !aligned16(W_o) ||
+      !aligned16(out) || !aligned16(W_kvb_scale) || !aligned16(W_o_scale) ||
+      ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(cache_len) |
+        reinterpret_cast<uintptr_t>(n_nodes) | reinterpret_cast<uintptr_t>(parents)) & 3u))
+    return MLA_ERR_ALIGN;
+  if (dims->act != MLA_ACT_BF16) return MLA_ERR_UNSUPPORTED;
+  rc = begin_call(dims, MLA_ENTRY_TREE_DECODE, false, workspace, ws_bytes, &ds, &lay);
+  if (rc != MLA_OK) return rc;
+  return run_tree_decode(ds, *dims, *pages, lay, workspace, q, kv_cache, k_pe_cache, block_table, cache_len, n_nodes,
+                         parents, W_kvb, W_kvb_scale, W_o, W_o_scale, scale, out,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mla_cache_compact(const mla_pages* pages, void* kv_cache, void* k_pe_cache, const int32_t* block_table,
+                      const int32_t* cache_len, const int32_t* accepted, const int32_t* n_accepted, int B, int width,
+                      mla_stream_t stream) {
+  int rc = check_pages(pages, true);
+  if (rc != MLA_OK) return rc;
+  if (B < 0 || width < 0 || width > MLA_MAX_TREE) return MLA_ERR_SHAPE;
+  if (B == 0 || width == 0 || pages->num_pages == 0) return MLA_OK;
+  if (!kv_cache || !k_pe_cache || !block_table || !cache_len || !accepted || !n_accepted) return MLA_ERR_NULL;
+  if (!aligned16(kv_cache) || !aligned16(k_pe_cache) ||
+      ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(cache_len) |
+        reinterpret_cast<uintptr_t>(accepted) | reinterpret_cast<uintptr_t>(n_accepted)) & 3u))
+    return MLA_ERR_ALIGN;
+  DeviceState* ds = nullptr;
+  if ((rc = device_state(&ds)) != MLA_OK) return rc;
+  mla::CompactParams p;
+  p.kv = static_cast<uint4*>(kv_cache);
+  p.pe = static_cast<uint4*>(k_pe_cache);
+  p.num_pages = pages->num_pages;
+  p.page_shift = log2_of(pages->page_size);
+  p.table_width = pages->table_width;
+  p.table = block_table;
+  p.cache_len = cache_len;
+  p.accepted = accepted;
+  p.counts = n_accepted;
+  p.width = width;
+  p.err = ds->err;
+  const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>(pages->layers));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // Rows a thread holds: 2, 4 or 16, by the most that a sequence can accept.
+  if (width <= 2 * mla::kCompactRows)
+    mla::cache_compact_kernel<2><<<grid, mla::kCompactThreads, 0, st>>>(p);
+  else if (width <= 4 * mla::kCompactRows)
+    mla::cache_compact_kernel<4><<<grid, mla::kCompactThreads, 0, st>>>(p);
+  else
+    mla::cache_compact_kernel<MLA_MAX_TREE / mla::kCompactRows><<<grid, mla::kCompactThreads, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_cache_copy_pages(const mla_pages* pages, void* kv_cache, void* k_pe_cache, const int32_t* src,
+                         const int32_t* dst, int n, mla_stream_t stream) {
+  int rc = check_pages(pages, false);
+  if (rc != MLA_OK) return rc;
+  if (n < 0) return MLA_ERR_SHAPE;
+  if (n == 0) return MLA_OK;
+  if (!kv_cache || !k_pe_cache || !src || !dst) return MLA_ERR_NULL;
+  if (!aligned16(kv_cache) || !aligned16(k_pe_cache)) return MLA_ERR_ALIGN;
+  for (int i = 0; i < n; ++i)
+    if (src[i] < 0 || src[i] >= pages->num_pages || dst[i] < 0 || dst[i] >= pages->num_pages) return MLA_ERR_SHAPE;
+  // No destination twice, and none that another pair reads. A few pairs are
+  // compared with one another, many through one mark per page.
+  if (n <= 64) {
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < n; ++j)
+        if (i != j && (dst[i] == dst[j] || dst[i] == src[j])) return MLA_ERR_SHAPE;
+  } else {
+    int* owner = new (std::nothrow) int[pages->num_pages];
+    if (owner == nullptr) return MLA_ERR_CUDA;
+    for (int i = 0; i < pages->num_pages; ++i) owner[i] = -1;
+    bool ok = true;
+    for (int i = 0; i < n && ok; ++i) {
+      ok = owner[dst[i]] < 0;
+      owner[dst[i]] = i;
+    }
+    for (int i = 0; i < n && ok; ++i) ok = owner[src[i]] < 0 || owner[src[i]] == i;
+    delete[] owner;
+    if (!ok) return MLA_ERR_SHAPE;
+  }
+  DeviceState* ds = nullptr;
+  if ((rc = device_state(&ds)) != MLA_OK) return rc;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int per = mla::kCopyThreads * mla::kCopyPer;
+  const unsigned pieces = static_cast<unsigned>((int64_t(pages->page_size) * mla::kRowPieces + per - 1) / per);
+  mla::PagePairs pp;
+  for (int i = 0; i < n;) {
+    int k = 0;
+    for (; i < n && k < mla::kCopyPairs; ++i) {
+      if (src[i] == dst[i]) continue;
+      pp.src[k] = src[i];
+      pp.dst[k] = dst[i];
+      ++k;
+    }
+    if (k == 0) break;
+    mla::cache_copy_kernel<<<dim3(pieces, static_cast<unsigned>(k), static_cast<unsigned>(pages->layers)),
+                             mla::kCopyThreads, 0, st>>>(pp, static_cast<uint4*>(kv_cache),
+                                                         static_cast<uint4*>(k_pe_cache), pages->num_pages,
+                                                         pages->page_size);
+    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  }
+  return MLA_OK;
 }
 
 const char* mla_status_str(int status) {

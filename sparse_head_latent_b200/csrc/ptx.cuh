@@ -19,6 +19,8 @@ enum : int {
   kErrWaitSoftmax = 105,  // a wait for the softmax warps timed out
   kErrGeometry = 201,     // launch geometry does not match the kernel's assumptions
   kErrRangeF16 = 301,     // an up-projected v exceeded the f16 range of the attention path
+  kErrPage = 401,         // a needed entry of a block table (or an accepted node) lies outside the cache
+  kErrLength = 402,       // a sequence's positions do not fit its row of the block table
 };
 
 // Magnitude from which fp32 -> f16 rounding (nearest even) gives infinity:

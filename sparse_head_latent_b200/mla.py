@@ -7,6 +7,7 @@ the first call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -19,6 +20,7 @@ _lock = threading.Lock()
 _lib = None
 
 MLA_ENTRY_KV_UPPROJECT, MLA_ENTRY_ATTEND, MLA_ENTRY_OUT_PROJECT, MLA_ENTRY_PREFILL, MLA_ENTRY_DECODE = 0, 1, 2, 3, 4
+MLA_ENTRY_TREE_DECODE = 5
 MLA_W_BF16, MLA_W_E4M3_BLOCK128 = 0, 1
 MLA_PROFILE_CLASSES = 10
 MLA_PATH_AUTO, MLA_PATH_BLOCK_DENSE, MLA_PATH_ABSORBED = 0, 1, 2
@@ -26,6 +28,9 @@ MLA_ACT_BF16, MLA_ACT_E4M3_DYNAMIC = 0, 1
 PROFILE_CLASS_NAMES = ("topk_prepass", "weight_dequant", "gemm_kvb", "attention", "gemm_wo", "row_lists",
                        "gemm_absorb", "attention_absorbed", "act_quant", "gemm_wo_split_sum")
 D_NOPE, D_ROPE, D_V, D_LATENT, D_MODEL = 128, 64, 128, 512, 7168
+MLA_ROPE_INTERLEAVED, MLA_ROPE_HALF = 0, 1
+MLA_ROPE_UNSCALED, MLA_ROPE_LINEAR, MLA_ROPE_YARN = 0, 1, 2
+MLA_MAX_TREE = 64
 
 
 class MlaDims(ctypes.Structure):
@@ -33,6 +38,15 @@ class MlaDims(ctypes.Structure):
                 ("d_nope", ctypes.c_int), ("d_rope", ctypes.c_int), ("d_v", ctypes.c_int),
                 ("d_latent", ctypes.c_int), ("d_model", ctypes.c_int),
                 ("topk", ctypes.c_int), ("wdtype", ctypes.c_int), ("path", ctypes.c_int), ("act", ctypes.c_int)]
+
+
+class MlaRopeTable(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_uint64 * (D_ROPE // 2)), ("magnitude", ctypes.c_float), ("layout", ctypes.c_int)]
+
+
+class MlaPages(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("table_width", ctypes.c_int),
+                ("layers", ctypes.c_int)]
 
 
 class MlaError(RuntimeError):
@@ -56,6 +70,19 @@ SIGNATURES = {
     "mla_attend_static": (ctypes.c_int, [ctypes.POINTER(MlaDims), _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_float,
                                          _VP, _VP]),
     "mla_quantize_act": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.c_int, _VP, _VP, _VP]),
+    "mla_rope_init": (ctypes.c_int, [ctypes.POINTER(MlaRopeTable), ctypes.c_int, ctypes.c_double, ctypes.c_int,
+                                     ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                     ctypes.c_float]),
+    "mla_rope": (ctypes.c_int, [ctypes.POINTER(MlaRopeTable), _VP, ctypes.c_longlong, ctypes.c_longlong, _VP,
+                                ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                ctypes.c_int, _VP, ctypes.c_int, _VP]),
+    "mla_cache_append": (ctypes.c_int, [ctypes.POINTER(MlaRopeTable), _VP, ctypes.c_longlong, _VP, ctypes.c_int,
+                                        ctypes.c_float, _VP, _VP, ctypes.c_int, _VP, _VP, ctypes.c_longlong, _VP]),
+    "mla_tree_decode": (ctypes.c_int, [ctypes.POINTER(MlaDims), ctypes.POINTER(MlaPages), _VP, _VP, _VP, _VP, _VP,
+                                       _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_float, _VP, _VP, _SZ, _VP]),
+    "mla_cache_compact": (ctypes.c_int, [ctypes.POINTER(MlaPages), _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int,
+                                         ctypes.c_int, _VP]),
+    "mla_cache_copy_pages": (ctypes.c_int, [ctypes.POINTER(MlaPages), _VP, _VP, _VP, _VP, ctypes.c_int, _VP]),
     "mla_status_str": (ctypes.c_char_p, [ctypes.c_int]),
     "mla_device_status": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_int)]),
     "mla_set_e4m3_weight_conversion": (ctypes.c_int, [ctypes.c_int]),
@@ -263,6 +290,234 @@ def mla_quantize_act(x, codes=None, scales=None, stream=None):
     _check("mla_quantize_act", load_library().mla_quantize_act(_ptr(x), rows, cols, _ptr(codes), _ptr(scales),
                                                                _stream(stream)))
     return codes, scales
+
+
+# ------------------------------------------------------------------ serving over a paged cache
+
+
+def _expect(t, name, dtype, shape=None):
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+
+
+def _call(name, device, stream, args, used=()):
+    """Runs an entry point on the tensors' device, on `stream` or that device's current stream. `used`: tensors
+    allocated here, which the caching allocator must not hand out again before `stream` is done with them."""
+    if device.type != "cuda":
+        raise ValueError("tensor must be on a CUDA device")
+    fn = getattr(_lib or load_library(), name)
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        for t in used:
+            t.record_stream(stream)
+    else:
+        stream = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream.cuda_stream)
+    _check(name, rc)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def make_rope(base=10000.0, layout=MLA_ROPE_INTERLEAVED, scaling=MLA_ROPE_UNSCALED, factor=1.0, original_len=4096,
+              beta_fast=32.0, beta_slow=1.0, magnitude=1.0) -> MlaRopeTable:
+    """Rotary settings of a model (the frequencies of the 32 pairs, scaled for long contexts), made once and
+    passed to mla_rope and mla_cache_append."""
+    table = MlaRopeTable()
+    _check("mla_rope_init", load_library().mla_rope_init(
+        ctypes.byref(table), int(layout), float(base), int(scaling), float(factor), float(original_len),
+        float(beta_fast), float(beta_slow), float(magnitude)))
+    return table
+
+
+def _rows_and_heads(t, lead):
+    """(rows, row stride, heads, head stride) of a tensor [*lead, H, W] or [*lead, W] whose last dimension is
+    contiguous and whose leading ones fold into one."""
+    if t.dim() not in (lead + 1, lead + 2) or t.stride(-1) != 1:
+        raise ValueError("the tensor must be [*positions.shape, heads, width] or [*positions.shape, width], its last "
+                         "dimension contiguous")
+    heads, head_stride = (t.shape[-2], t.stride(-2)) if t.dim() == lead + 2 else (1, t.shape[-1])
+    rows, stride = 1, 0
+    for d in reversed(range(lead)):
+        if t.shape[d] == 1:
+            continue
+        if rows == 1:
+            stride = t.stride(d)
+        elif t.stride(d) != stride * rows:
+            raise ValueError("the leading dimensions must fold into one")
+        rows *= t.shape[d]
+    return rows, stride, heads, head_stride
+
+
+def mla_rope(x, positions, rope, offset=None, out=None, inverse=False, stream=None):
+    """Rotates 64 elements of every head by its token's position: x bf16 [*positions.shape, H, W] (or without H),
+    positions int32; elements [offset, offset + 64) (default: the last 64) are turned, the others copied. `out` may be
+    x (in place). Strided x and out are taken as they are. inverse=True rotates back (the transposed map: with
+    x = d out, the gradient). `rope` comes from make_rope."""
+    _expect(x, "x", torch.bfloat16)
+    _expect(positions, "positions", torch.int32)
+    lead = positions.dim()
+    rows, x_row, heads, x_head = _rows_and_heads(x, lead)
+    if x.shape[:lead] != positions.shape:
+        raise ValueError(f"x {tuple(x.shape)} does not start with the shape of positions {tuple(positions.shape)}")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        used = (out,)
+    else:
+        _expect(out, "out", torch.bfloat16, tuple(x.shape))
+        used = ()
+    _same_device(x.device, positions=positions, out=out)
+    _, o_row, _, o_head = _rows_and_heads(out, lead)
+    width = x.shape[-1]
+    _call("mla_rope", x.device, stream,
+          (ctypes.byref(rope), x.data_ptr(), x_row, x_head, out.data_ptr(), o_row, o_head, rows, heads, width,
+           width - D_ROPE if offset is None else int(offset), _ptr(positions), 1 if inverse else 0), used)
+    return out
+
+
+def mla_cache_append(kv_a, norm_weight, positions, rope, kv_cache, k_pe_cache, slots=None, eps=1e-6, stream=None):
+    """Latent RMSNorm and key rotation in one pass, into cache rows: kv_a bf16 [*positions.shape, 576] (rows may be
+    strided), norm_weight bf16 or float32 [512], positions int32; slots int32, one cache row per token (-1: skip), or
+    None: token r to row r. kv_cache bf16 [..., 512] and k_pe_cache bf16 [..., 64] are contiguous with the same number
+    of rows (pages [P, page, 512], or mla_prefill's kv_latent [B, T, 512]). Returns (kv_cache, k_pe_cache)."""
+    _expect(kv_a, "kv_a", torch.bfloat16)
+    _expect(positions, "positions", torch.int32)
+    _expect(kv_cache, "kv_cache", torch.bfloat16)
+    _expect(k_pe_cache, "k_pe_cache", torch.bfloat16)
+    if norm_weight.dtype not in (torch.bfloat16, torch.float32) or tuple(norm_weight.shape) != (D_LATENT,):
+        raise ValueError("norm_weight must be bf16 or float32 [512]")
+    if kv_a.shape != (*positions.shape, D_LATENT + D_ROPE):
+        raise ValueError("kv_a must be [*positions.shape, 576]")
+    rows, stride, _, _ = _rows_and_heads(kv_a, positions.dim())
+    if rows <= 1:
+        stride = D_LATENT + D_ROPE
+    if slots is not None:
+        _expect(slots, "slots", torch.int32, tuple(positions.shape))
+    if kv_cache.shape[-1] != D_LATENT or k_pe_cache.shape != (*kv_cache.shape[:-1], D_ROPE):
+        raise ValueError("kv_cache must be [..., 512] and k_pe_cache [..., 64] over the same rows")
+    cache_rows = kv_cache.numel() // D_LATENT
+    if slots is None and cache_rows < rows:
+        raise ValueError("the cache has fewer rows than there are tokens")
+    _same_device(kv_a.device, norm_weight=norm_weight, positions=positions, slots=slots, kv_cache=kv_cache,
+                 k_pe_cache=k_pe_cache)
+    _call("mla_cache_append", kv_a.device, stream,
+          (ctypes.byref(rope), kv_a.data_ptr(), stride, _ptr(norm_weight),
+           1 if norm_weight.dtype == torch.float32 else 0, float(eps), _ptr(positions), _ptr(slots), rows,
+           _ptr(kv_cache), _ptr(k_pe_cache), cache_rows))
+    return kv_cache, k_pe_cache
+
+
+def _pages(kv_cache, k_pe_cache, table_width, one_layer):
+    _expect(kv_cache, "kv_cache", torch.bfloat16)
+    _expect(k_pe_cache, "k_pe_cache", torch.bfloat16)
+    shape = kv_cache.shape
+    if len(shape) not in ((3,) if one_layer else (3, 4)) or shape[-1] != D_LATENT:
+        raise ValueError("kv_cache must be [pages, page_size, 512]" +
+                         ("" if one_layer else " or [layers, pages, page_size, 512]"))
+    if k_pe_cache.shape != (*shape[:-1], D_ROPE):
+        raise ValueError("k_pe_cache must be [..., 64] over kv_cache's pages")
+    return MlaPages(shape[-3], shape[-2], table_width, shape[0] if len(shape) == 4 else 1)
+
+
+def mla_tree_decode(q, kv_cache, k_pe_cache, block_table, cache_len, W_kvb, W_o, W_kvb_scale=None, W_o_scale=None,
+                    parents=None, n_nodes=None, scale=192 ** -0.5, out=None, workspace=None, stream=None):
+    """Attention of up to 64 new tokens per sequence over a paged cache, and W_o: q bf16 [B, N, H, 192], kv_cache
+    [pages, page_size, 512], k_pe_cache [pages, page_size, 64], block_table int32 [B, width], cache_len int32 [B]
+    (committed positions; node j of a sequence is cached at position cache_len + j), n_nodes int32 [B] or None (all N),
+    parents int32 [B, N] (the node each hangs below, -1: the last committed position) or None: a chain
+    -> out bf16 [B, N, 7168], 0 for nodes from n_nodes on."""
+    _expect(q, "q", torch.bfloat16)
+    if q.dim() != 4 or q.shape[-1] != D_NOPE + D_ROPE:
+        raise ValueError("q must be [B, N, H, 192]")
+    B, N, H, _ = q.shape
+    _expect(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, width]")
+    _expect(cache_len, "cache_len", torch.int32, (B,))
+    if n_nodes is not None:
+        _expect(n_nodes, "n_nodes", torch.int32, (B,))
+    if parents is not None:
+        _expect(parents, "parents", torch.int32, (B, N))
+    fp8 = _wtype(W_kvb)
+    if _wtype(W_o) != fp8:
+        raise ValueError("W_kvb and W_o must use the same storage type")
+    if tuple(W_kvb.shape) != (H * (D_NOPE + D_V), D_LATENT) or tuple(W_o.shape) != (H * D_V, D_MODEL):
+        raise ValueError("W_kvb must be [H*256, 512] and W_o [H*128, 7168]")
+    if fp8:
+        for w, s, name in ((W_kvb, W_kvb_scale, "W_kvb_scale"), (W_o, W_o_scale, "W_o_scale")):
+            if s is None:
+                raise ValueError(f"e4m3 weights need {name}")
+            _expect(s, name, torch.float32, (w.shape[0] // 128, w.shape[1] // 128))
+    pages = _pages(kv_cache, k_pe_cache, block_table.shape[1], True)
+    _same_device(q.device, kv_cache=kv_cache, k_pe_cache=k_pe_cache, block_table=block_table, cache_len=cache_len,
+                 W_kvb=W_kvb, W_o=W_o, W_kvb_scale=W_kvb_scale, W_o_scale=W_o_scale, parents=parents,
+                 n_nodes=n_nodes, out=out, workspace=workspace)
+    dims = make_dims(B, N, H, 0, fp8)
+    used = []
+    if out is None:
+        out = torch.empty(B, N, D_MODEL, dtype=torch.bfloat16, device=q.device)
+        used.append(out)
+    else:
+        _expect(out, "out", torch.bfloat16, (B, N, D_MODEL))
+    own_ws = workspace is None
+    ws, nbytes = _workspace(dims, MLA_ENTRY_TREE_DECODE, False, workspace, q.device)
+    if own_ws:
+        used.append(ws)
+    _call("mla_tree_decode", q.device, stream,
+          (ctypes.byref(dims), ctypes.byref(pages), _ptr(q), _ptr(kv_cache), _ptr(k_pe_cache), _ptr(block_table),
+           _ptr(cache_len), _ptr(n_nodes), _ptr(parents), _ptr(W_kvb), _ptr(W_kvb_scale), _ptr(W_o), _ptr(W_o_scale),
+           float(scale), _ptr(out), _ptr(ws), nbytes), used)
+    return out
+
+
+def mla_cache_compact(kv_cache, k_pe_cache, block_table, cache_len, accepted, n_accepted, stream=None):
+    """Moves each sequence's accepted rows together: position cache_len + accepted[b, i] to cache_len + i for
+    i < n_accepted[b], in every layer. kv_cache [pages, page_size, 512] or [layers, pages, page_size, 512] (k_pe_cache
+    alike with 64), accepted int32 [B, width <= 64], the others int32 [B]."""
+    pages = _pages(kv_cache, k_pe_cache, block_table.shape[-1], False)
+    _expect(block_table, "block_table", torch.int32)
+    _expect(accepted, "accepted", torch.int32)
+    if block_table.dim() != 2 or accepted.dim() != 2:
+        raise ValueError("block_table and accepted must be [B, width]")
+    B = block_table.shape[0]
+    _expect(cache_len, "cache_len", torch.int32, (B,))
+    _expect(accepted, "accepted", torch.int32, (B, accepted.shape[1]))
+    _expect(n_accepted, "n_accepted", torch.int32, (B,))
+    _same_device(kv_cache.device, k_pe_cache=k_pe_cache, block_table=block_table, cache_len=cache_len,
+                 accepted=accepted, n_accepted=n_accepted)
+    _call("mla_cache_compact", kv_cache.device, stream,
+          (ctypes.byref(pages), _ptr(kv_cache), _ptr(k_pe_cache), _ptr(block_table), _ptr(cache_len), _ptr(accepted),
+           _ptr(n_accepted), B, accepted.shape[1]))
+
+
+def mla_cache_copy_pages(kv_cache, k_pe_cache, src, dst, stream=None):
+    """Copies page src[i] onto page dst[i] in every layer. src and dst are host lists (sequences of ints or int32 CPU
+    tensors) of equal length; a destination may be listed once and be no other pair's source. The caches are as for
+    mla_cache_compact."""
+    n = len(src)
+    if len(dst) != n:
+        raise ValueError("src and dst must have the same length")
+    lists = []
+    for v in (src, dst):
+        if isinstance(v, torch.Tensor):
+            if v.is_cuda:
+                raise ValueError("src and dst are host lists, not CUDA tensors")
+            v = v.tolist()
+        lists.append(array.array("i", v))  # OverflowError for an index beyond 32 bits
+    pages = _pages(kv_cache, k_pe_cache, 0, False)
+    _same_device(kv_cache.device, k_pe_cache=k_pe_cache)
+    _call("mla_cache_copy_pages", kv_cache.device, stream,
+          (ctypes.byref(pages), _ptr(kv_cache), _ptr(k_pe_cache), lists[0].buffer_info()[0], lists[1].buffer_info()[0], n))
 
 
 def mla_device_status(stream=None) -> int:
