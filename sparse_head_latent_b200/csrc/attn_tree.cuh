@@ -8,27 +8,66 @@
 //   z_t      = scale [q_abs | q_pe] . [c_t | k_pe_t]     (576 wide)
 //   o_lat    = sum_t softmax(z)_t c_t
 // per (node, head); q_abs = q_nope W_UK before, attn = W_UV o_lat after it.
+//
+// All (node, head) rows of a sequence meet the same keys, so they are the rows
+// of one matrix product: tiles of 128 rows (H = 128: one node a tile) against
+// blocks of 128 keys. Work item: one CTA pair per run of consecutive (tile,
+// block) units; the units of all sequences, tile after tile, are cut into
+// equal shares, one per resident pair, so that ragged lengths, one long
+// sequence and many short ones all fill the machine. A tile that several pairs
+// share is joined by tree_combine_kernel.
+//
+// Shape of the products. A pair UMMA with M = 128 gives each CTA 64 rows and
+// uses all 128 lanes of its tensor memory: lanes 0..63 hold columns [0, N/2) of
+// rows 0..63, lanes 64..127 columns [N/2, N). O (64 rows x 512 fp32) then takes
+// 256 of the 512 columns, where 128 rows in one CTA would take all of them
+// and leave none for S. Measured rates of the tensor core alone (clk per block
+// of 128 keys; full rate in brackets): P.V 1050 (1024); Q.K^T 1877 (1152) with
+// Q from shared memory; both together 2600 (2176).
+//
+// Shared memory per CTA: P (64 rows x 128 keys), Q, a rope slot and a ring of
+// units of four [64 keys x 64] slots. For Q.K^T a CTA holds its own 64 of the
+// block's keys, all 576 values of each; for P.V all 128 keys, its own 128 of
+// each 256 values. The two meet in place: unit h (values [256 h, 256 h + 256))
+// holds the own keys' four 64-value chunks; once Q.K^T has read it, the two
+// slots with values the CTA does not need are loaded again with the other
+// keys' chunks it does need (CTA 0: slots 2, 3 from the other 64 keys; CTA 1:
+// slots 0, 1). So slots 0, 1 always hold keys 0..63 and slots 2, 3 keys
+// 64..127 for P.V in both CTAs, and a key's row crosses L2 -> SM 13/9 times
+// instead of 17/9.
+//
+// Roles (320 threads per CTA): warp 0 producer; warp 1 issues the UMMAs
+// (leader) or forwards "P is written" (the other CTA); warps 2..9 softmax: four
+// threads per row, one for each quarter of the block's keys, agree on the
+// running maximum through shared memory.
 #pragma once
 
+#include "gemm2.cuh"
 #include "ptx.cuh"
 
 namespace mla {
 
-constexpr int kTreeMax = 64;  // nodes per sequence: one bit each
+constexpr int kTreeMax = 64;        // nodes per sequence: one bit each
+constexpr int kTreeRows = 128;      // rows of a tile
+constexpr int kTreeBlock = 128;     // keys of a block
+constexpr int kTreeMaxPairs = 74;   // pairs a launch uses at most (148 SMs); the workspace is sized for them
+constexpr int kTreeThreads = 320;
+constexpr int kTreeSlotFloats = kTreeRows * 512;  // one partial tile
 
 struct TreeParams {
   int B, N, H;
   int num_pages, page_shift, table_width;
+  int box_shift;                 // log2 of the keys per TMA box: min(page, 64)
   float scale_log2;              // softmax scale * log2(e)
   const int32_t* table;          // [B][table_width]
   const int32_t* cache_len;      // [B]
   const int32_t* n_nodes;        // [B], or nullptr: N each
   const int32_t* parents;        // [B][N], or nullptr: a chain
   const __nv_bfloat16* qabs;     // [B*N][H][512]
-  const __nv_bfloat16* q;        // [B*N][H][192] (rope at 128..191)
-  const __nv_bfloat16* kv;       // [num_pages * page][512]
-  const __nv_bfloat16* pe;       // [num_pages * page][64]
   __nv_bfloat16* olat;           // [B*N][H][512]
+  int64_t* ustart;               // [B + 1] first unit of each sequence, and their number
+  float* part_o;                 // [2 pairs][128 value quads][128 rows][4] unnormalised partial tiles
+  float2* part_ml;               // [2 pairs][128 rows] (max in the scaled log2 domain, sum)
   int* err;
 };
 
@@ -43,89 +82,643 @@ __device__ __forceinline__ void tree_lengths(const TreeParams& p, int b, int& le
   }
 }
 
-constexpr int kTreeKeys = 32;
-constexpr int kTreeWarps = 8;
+__device__ __forceinline__ void tree_extent(const TreeParams& p, int len, int nodes, int& tiles, int& blocks) {
+  tiles = (nodes * p.H + kTreeRows - 1) / kTreeRows;
+  blocks = nodes > 0 ? (len + nodes + kTreeBlock - 1) / kTreeBlock : 0;
+}
 
-// One warp per (node, head), eight heads of a node per block; the block
-// stages 32 positions at a time.
-__global__ void __launch_bounds__(32 * kTreeWarps)
-tree_attn_kernel(const TreeParams p) {
-  __shared__ __align__(16) __nv_bfloat16 keys[kTreeKeys][576 + 8];
-  __shared__ __nv_bfloat16 qs[kTreeWarps][576];
-  const int hg = (p.H + kTreeWarps - 1) / kTreeWarps;
-  const int node_row = blockIdx.x / hg, b = node_row / p.N, j = node_row % p.N;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = (blockIdx.x % hg) * kTreeWarps + warp;
-  int len, nodes;
-  tree_lengths(p, b, len, nodes);
-  const int64_t qrow = static_cast<int64_t>(node_row) * p.H + min(h, p.H - 1);
-  float acc[16], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  if (j < nodes) {
-    uint64_t sees = 1ull << j;
-    if (p.parents) {
-      int k = j;
-      while (true) {
-        const int up = __ldg(p.parents + static_cast<int64_t>(b) * p.N + k);
-        if (up < 0 || up >= k) break;
-        sees |= 1ull << up;
-        k = up;
-      }
-    } else {
-      sees |= (1ull << j) - 1;
+// A pair's next run of blocks [j0, j1) of one tile.
+struct TreeSeg {
+  int b, tile, j0, j1, len, nodes, blocks;
+  bool first;  // the pair's first run
+};
+
+// Walks a pair's share [u, u1) of the units; every role walks it alike.
+struct TreeWork {
+  int64_t u0, u, u1, base;  // base: first unit of sequence b
+  int b;
+  __device__ bool next(const TreeParams& p, TreeSeg& s) {
+    if (u >= u1) return false;
+    int tiles;
+    while (true) {
+      tree_lengths(p, b, s.len, s.nodes);
+      tree_extent(p, s.len, s.nodes, tiles, s.blocks);
+      const int64_t units = static_cast<int64_t>(tiles) * s.blocks;
+      if (u < base + units) break;
+      base += units;
+      ++b;
     }
-    for (int d = lane; d < 576; d += 32)
-      qs[warp][d] = d < 512 ? p.qabs[qrow * 512 + d] : p.q[qrow * 192 + 128 + d - 512];
-    const int T = len + nodes;
-    for (int t0 = 0; t0 < T; t0 += kTreeKeys) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < kTreeKeys * 72; i += 32 * kTreeWarps) {
-        const int r = i / 72, c = i % 72, t = t0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (t < T) {
-          const int page = __ldg(p.table + static_cast<int64_t>(b) * p.table_width + (t >> p.page_shift));
-          if (page >= 0 && page < p.num_pages) {
-            const int64_t row = (static_cast<int64_t>(page) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
-            v = __ldg(reinterpret_cast<const uint4*>(c < 64 ? p.kv + row * 512 + c * 8 : p.pe + row * 64 + (c - 64) * 8));
-          } else if (c == 0) {
-            atomicCAS(p.err, 0, kErrPage);
+    s.b = b;
+    s.tile = static_cast<int>((u - base) / s.blocks);
+    s.j0 = static_cast<int>((u - base) % s.blocks);
+    s.j1 = static_cast<int>(min(static_cast<int64_t>(s.blocks), s.j0 + (u1 - u)));
+    s.first = u == u0;
+    u += s.j1 - s.j0;
+    return true;
+  }
+};
+
+__host__ __device__ __forceinline__ int64_t tree_share(int64_t units, int pair, int pairs) {
+  return units * pair / pairs;
+}
+
+struct TreeSmem {
+  static constexpr int CHUNK = 8192;               // [64 keys or rows x 64] bf16
+  static constexpr int UNIT = 4 * CHUNK;
+  static constexpr int UNITS = 4;
+  static constexpr int Q_CHUNKS = 9;
+  static constexpr int RING = 0;
+  static constexpr int ROPE = RING + UNITS * UNIT;
+  static constexpr int Q = ROPE + CHUNK;
+  static constexpr int P = Q + Q_CHUNKS * CHUNK;   // two [64 rows x 64 keys] chunks
+  static constexpr int XCHG = P + 2 * CHUNK;       // [2][4][64] floats
+  static constexpr int BARS = XCHG + 2 * 4 * 64 * 4;
+  static constexpr int BYTES = BARS + 512;
+};
+static_assert(TreeSmem::BYTES <= 232448, "shared memory per CTA");
+
+// Barriers; (L): only the leader's copy is used, by both CTAs.
+enum : int {
+  kTreeKFull = 0,                             // (L) per unit: the own keys' chunks landed in both CTAs
+  kTreeVFull = kTreeKFull + TreeSmem::UNITS,  // (L) per unit: the other keys' chunks landed in both CTAs
+  kTreeEmpty = kTreeVFull + TreeSmem::UNITS,  // per unit: the P.V that read it is done
+  kTreeSFull = kTreeEmpty + TreeSmem::UNITS,  // per S buffer: Q.K^T of a block is done
+  kTreePVDone = kTreeSFull + 2,               // P.V of a block is done
+  kTreeRopeFull,                              // (L) the rope slot landed in both CTAs
+  kTreeQFull,                                 // (L) Q landed in both CTAs
+  kTreePLocal,                                // (the other CTA) its eight warps have written P
+  kTreePFull,                                 // (L) P of both CTAs is written
+  kTreeTail,                                  // the other keys' chunks of a block with drafted keys landed in this CTA
+  kTreeDrain,
+  kTreeBars
+};
+
+constexpr uint32_t kTreeColS = 256;  // S buffers at 256 and 320; O at 0 and 128
+
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Nodes that node j of sequence b sees, as bits (itself included); every lane
+// of the warp asks for its own j. The parents of nodes `lane` and `lane + 32`
+// are in registers; six rounds double the distance looked up.
+__device__ __forceinline__ uint64_t tree_ancestors(const TreeParams& p, int b, int j) {
+  if (p.parents == nullptr) return j < kTreeMax ? (j == 63 ? ~0ull : (2ull << j) - 1) : 0ull;
+  const int lane = static_cast<int>(lane_id());
+  uint64_t sees[2];
+  int up[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = lane + 32 * i;
+    sees[i] = 1ull << k;
+    const int v = k < p.N ? __ldg(p.parents + static_cast<int64_t>(b) * p.N + k) : -1;
+    up[i] = v >= 0 && v < k ? v : -1;
+  }
+#pragma unroll 1
+  for (int round = 0; round < 6; ++round) {
+    uint64_t s2[2];
+    int u2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int from = max(up[i], 0);
+      const uint64_t a = __shfl_sync(0xffffffffu, sees[0], from & 31), c = __shfl_sync(0xffffffffu, sees[1], from & 31);
+      const int d = __shfl_sync(0xffffffffu, up[0], from & 31), e = __shfl_sync(0xffffffffu, up[1], from & 31);
+      s2[i] = up[i] < 0 ? 0ull : from < 32 ? a : c;
+      u2[i] = up[i] < 0 ? -1 : from < 32 ? d : e;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sees[i] |= s2[i];
+      up[i] = u2[i];
+    }
+  }
+  const uint64_t a = __shfl_sync(0xffffffffu, sees[0], j & 31), c = __shfl_sync(0xffffffffu, sees[1], j & 31);
+  return j < 32 ? a : j < kTreeMax ? c : 0ull;
+}
+
+// Which of the 32 keys from position t0 on a row sees, as bits.
+__device__ __forceinline__ uint32_t tree_keep(int64_t t0, int len, uint64_t sees) {
+  const int64_t d = t0 - len;
+  if (d >= kTreeMax) return 0u;
+  if (d >= 0) return static_cast<uint32_t>(sees >> d);
+  if (d <= -32) return ~0u;
+  return static_cast<uint32_t>(sees << -d) | ((1u << -d) - 1u);
+}
+
+__global__ void __launch_bounds__(kTreeThreads, 1)
+tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_pe,
+                 const __grid_constant__ CUtensorMap tm_qabs, const __grid_constant__ CUtensorMap tm_q,
+                 const TreeParams p) {
+  using S = TreeSmem;
+  // Every byte is in use, so the swizzle's 1024-byte alignment is the base's
+  // own (dynamic shared memory starts there without static shared memory).
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (blockDim.x != kTreeThreads || (smem_u32(smem) & 1023u) != 0u) {
+    if (threadIdx.x == 0) atomicCAS(p.err, 0, kErrGeometry);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BARS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kTreeBars);
+  int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
+  int64_t* start = reinterpret_cast<int64_t*>(smem + S::BARS + 384);  // units, first unit of the share's sequence, it
+  const uint32_t bar0 = smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTreeBars; ++i) mbar_init(bar(i), i == kTreePLocal ? 8 : i == kTreePFull ? 9 : 1);
+    *abort_word = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm_kv);
+    prefetch_tmap(&tm_pe);
+    prefetch_tmap(&tm_qabs);
+    prefetch_tmap(&tm_q);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  // The share: units of all sequences, scanned by the whole CTA, each thread
+  // a run of sequences.
+  TreeWork work;
+  {
+    int64_t* sums = reinterpret_cast<int64_t*>(smem + S::XCHG);
+    const int per = (p.B + kTreeThreads - 1) / kTreeThreads;
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      int len, nodes, tiles, blocks;
+      tree_lengths(p, b, len, nodes);
+      tree_extent(p, len, nodes, tiles, blocks);
+      mine += static_cast<int64_t>(tiles) * blocks;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < kTreeThreads / 32; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    int64_t at = before + incl - mine;
+    const int64_t u0 = tree_share(total, pair, pairs);
+    const bool mark = blockIdx.x == 0, here = u0 >= at && u0 < at + mine;
+    if (mark || here) {
+      for (int b = b0; b < b1; ++b) {
+        int len, nodes, tiles, blocks;
+        tree_lengths(p, b, len, nodes);
+        tree_extent(p, len, nodes, tiles, blocks);
+        const int64_t units = static_cast<int64_t>(tiles) * blocks;
+        if (mark) p.ustart[b] = at;
+        if (u0 >= at && u0 < at + units) {
+          start[0] = at;
+          start[1] = b;
+        }
+        at += units;
+      }
+    }
+    if (mark && threadIdx.x == 0) p.ustart[p.B] = total;
+    work.u0 = work.u = u0;
+    work.u1 = tree_share(total, pair + 1, pairs);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrival
+  tc_fence_after();
+  work.base = start[0];
+  work.b = static_cast<int>(start[1]);
+  const uint32_t tmem = *tmem_slot;
+  const Abort ab{abort_word, p.err};
+  TreeSeg sg = {};
+
+  if (warp == 0) {
+    // ---------------- producer: the whole warp, each lane at most one box at a time
+    const int boxes = 64 >> p.box_shift;  // per 64 keys
+    const int cache_rows = p.num_pages << p.page_shift;
+    const uint32_t ring = smem_u32(smem + S::RING);
+    bool ok = true;
+    int g = 0;
+    // Cache row of box `lane` (of 2 * boxes) of block j; a box behind the last
+    // position reads zeros from behind the cache.
+    auto rows_of = [&](int j) -> int {
+      const int64_t t = static_cast<int64_t>(j) * kTreeBlock + (static_cast<int64_t>(lane) << p.box_shift);
+      if (lane >= 2 * boxes || j >= sg.blocks || t >= sg.len + sg.nodes) return cache_rows;
+      const int page = __ldg(p.table + static_cast<int64_t>(sg.b) * p.table_width + (t >> p.page_shift));
+      if (page < 0 || page >= p.num_pages) {
+        atomicCAS(p.err, 0, kErrPage);
+        return cache_rows;
+      }
+      return (page << p.page_shift) + static_cast<int>(t & ((int64_t(1) << p.page_shift) - 1));
+    };
+    // Loads four chunks' boxes of keys half `half` into slots slot0 .. : lane
+    // = chunk * boxes + box.
+    auto load_half = [&](int rows, int half, int chunk0, int chunks, uint32_t dst, uint32_t barrier, bool local) {
+      const int c = lane / boxes, x = lane % boxes;
+      const int row = __shfl_sync(0xffffffffu, rows, half * boxes + x);
+      if (c < chunks) {
+        const uint32_t d = dst + c * S::CHUNK + ((x << p.box_shift) << 7);
+        if (local)
+          tma_load_2d(d, &tm_kv, barrier, (chunk0 + c) * 64, row);
+        else
+          tma_load_2d_pair(d, &tm_kv, barrier, (chunk0 + c) * 64, row);
+      }
+    };
+    auto load_keys = [&](int block, int rows) -> bool {  // block: running index over the pair's blocks
+      for (int h = 0; h < 2; ++h) {
+        const int u = 2 * block + h, s = u % S::UNITS;
+        if (!warp_wait(bar(kTreeEmpty + s), ((u / S::UNITS) & 1) ^ 1, ab, kErrWaitConsumer)) return false;
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(kTreeKFull + s), 2 * S::UNIT);
+        __syncwarp();
+        load_half(rows, rank, 4 * h, 4, ring + s * S::UNIT, mapa_shared(bar(kTreeKFull + s), 0), false);
+      }
+      return true;
+    };
+    auto load_rope = [&](int rows) {
+      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(kTreeRopeFull), 2 * S::CHUNK);
+      __syncwarp();
+      const int row = __shfl_sync(0xffffffffu, rows, rank * boxes + lane % boxes);
+      if (lane < boxes)
+        tma_load_2d_pair(smem_u32(smem + S::ROPE) + ((lane << p.box_shift) << 7), &tm_pe,
+                         mapa_shared(bar(kTreeRopeFull), 0), 0, row);
+    };
+    while (ok && work.next(p, sg)) {
+      // Q: rows of this tile; those past the sequence's last belong to another
+      // sequence or to none, and are not stored. The previous run's products
+      // are done: its last block's S was waited for below.
+      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(kTreeQFull), 2 * S::Q_CHUNKS * S::CHUNK);
+      __syncwarp();
+      if (lane < S::Q_CHUNKS) {
+        const int qrow = (sg.b * p.N) * p.H + sg.tile * kTreeRows + 64 * rank;
+        const uint32_t d = smem_u32(smem + S::Q) + lane * S::CHUNK, qb = mapa_shared(bar(kTreeQFull), 0);
+        if (lane < 8)
+          tma_load_2d_pair(d, &tm_qabs, qb, lane * 64, qrow);
+        else
+          tma_load_2d_pair(d, &tm_q, qb, 128, qrow);
+      }
+      const int n = sg.j1 - sg.j0;
+      int r0 = rows_of(sg.j0), r1 = rows_of(sg.j0 + 1), r2 = rows_of(sg.j0 + 2);
+      ok = load_keys(g, r0);
+      if (ok) load_rope(r0);
+      if (ok && n > 1) ok = load_keys(g + 1, r1);
+      for (int j = 0; ok && j < n; ++j) {
+        const int r3 = j + 3 < n ? rows_of(sg.j0 + j + 3) : cache_rows;
+        const int block = g + j;
+        if (!(ok = warp_wait(bar(kTreeSFull + (block & 1)), (block >> 1) & 1, ab, kErrWaitMma))) break;
+        // The other keys' chunks, over the two slots of each unit this CTA is done with.
+        const bool tail = static_cast<int64_t>(sg.j0 + j + 1) * kTreeBlock > sg.len;
+        if (tail && lane == 0) mbar_arrive_expect_tx(bar(kTreeTail), 4 * S::CHUNK);
+        for (int h = 0; h < 2; ++h) {
+          const int u = 2 * block + h, s = u % S::UNITS;
+          if (rank == 0 && lane == 0) {
+            if (tail)
+              mbar_arrive(bar(kTreeVFull + s));  // "P is written" then tells that they landed, too
+            else
+              mbar_arrive_expect_tx(bar(kTreeVFull + s), 4 * S::CHUNK);
+          }
+          __syncwarp();
+          load_half(r0, 1 - rank, 4 * h + 2 * rank, 2, ring + s * S::UNIT + (rank == 0 ? 2 * S::CHUNK : 0),
+                    tail ? bar(kTreeTail) : mapa_shared(bar(kTreeVFull + s), 0), tail);
+        }
+        if (j + 1 < n) load_rope(r1);
+        if (j + 2 < n) ok = load_keys(block + 2, r2);
+        r0 = r1;
+        r1 = r2;
+        r2 = r3;
+      }
+      g += n;
+    }
+    if (!ok) spin_ns(2000000);  // let issued loads land before the CTA can exit
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---------------- UMMA issuer: Q.K^T of block j + 1, then P.V of block j
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 256, 0, 1);
+      const uint64_t dring = smem_desc_sw128(smem_u32(smem + S::RING), 16, 1024);
+      const uint64_t dring_mn = smem_desc_sw128(smem_u32(smem + S::RING), S::CHUNK, 1024);
+      const uint64_t drope = smem_desc_sw128(smem_u32(smem + S::ROPE), 16, 1024);
+      const uint64_t dq = smem_desc_sw128(smem_u32(smem + S::Q), 16, 1024);
+      const uint64_t dp = smem_desc_sw128(smem_u32(smem + S::P), 16, 1024);
+      bool ok = true;
+      int g = 0, seg = 0, commits = 0;
+      auto qk = [&](int block) -> bool {
+        const uint32_t ts = tmem + kTreeColS + 64u * static_cast<uint32_t>(block & 1);
+        for (int h = 0; h < 2; ++h) {
+          const int u = 2 * block + h, s = u % S::UNITS;
+          if (!mbar_wait(bar(kTreeKFull + s), (u / S::UNITS) & 1, ab, kErrWaitTma)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t in = ((i >> 2) * S::CHUNK + (i & 3) * 32) >> 4;
+            umma_ss_pair(ts, dq + ((h * S::UNIT) >> 4) + in, dring + ((s * S::UNIT) >> 4) + in, idesc_qk,
+                         (h > 0 || i > 0) ? 1u : 0u);
           }
         }
-        *reinterpret_cast<uint4*>(&keys[r][c * 8]) = v;
+        if (!mbar_wait(bar(kTreeRopeFull), block & 1, ab, kErrWaitTma)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          umma_ss_pair(ts, dq + ((8 * S::CHUNK + i * 32) >> 4), drope + ((i * 32) >> 4), idesc_qk, 1u);
+        umma_commit_pair(bar(kTreeSFull + (block & 1)), 0x3);
+        ++commits;
+        return true;
+      };
+      auto pv = [&](int block, bool fresh) -> bool {
+        if (!mbar_wait_cluster(bar(kTreePFull), block & 1, ab, kErrWaitSoftmax)) return false;
+        for (int h = 0; h < 2; ++h) {
+          const int u = 2 * block + h, s = u % S::UNITS;
+          if (!mbar_wait(bar(kTreeVFull + s), (u / S::UNITS) & 1, ab, kErrWaitTma)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ss_pair(tmem + 128u * h, dp + (((kk >> 2) * S::CHUNK + (kk & 3) * 32) >> 4),
+                         dring_mn + ((s * S::UNIT + (kk >> 2) * 2 * S::CHUNK + (kk & 3) * 2048) >> 4), idesc_pv,
+                         (!fresh || kk > 0) ? 1u : 0u);
+          umma_commit_pair(bar(kTreeEmpty + s), 0x3);
+        }
+        umma_commit_pair(bar(kTreePVDone), 0x3);
+        ++commits;
+        return true;
+      };
+      while (ok && work.next(p, sg)) {
+        const int n = sg.j1 - sg.j0;
+        if (!(ok = mbar_wait(bar(kTreeQFull), seg & 1, ab, kErrWaitTma))) break;
+        tc_fence_after();
+        ok = qk(g);
+        for (int j = 0; ok && j < n; ++j) {
+          if (j + 1 < n) ok = qk(g + j + 1);
+          if (ok) ok = pv(g + j, j == 0);
+        }
+        g += n;
+        ++seg;
       }
-      __syncthreads();
-      const int t = t0 + lane;
-      const bool seen = t < len || (t < T && ((sees >> (t - len)) & 1));
-      float z = 0.f;
-      for (int d = 0; d < 576; d += 2) {
-        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&keys[lane][d]));
-        z = fmaf(__bfloat162float(qs[warp][d]), f.x, fmaf(__bfloat162float(qs[warp][d + 1]), f.y, z));
+      if (!ok && commits > 0) {
+        umma_commit_pair(bar(kTreeDrain), 0x1);
+        mbar_wait_drain(bar(kTreeDrain), 0);
       }
-      z = seen ? z * p.scale_log2 : -INFINITY;
-      float top = z;
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float m_new = fmaxf(m, top);
-      if (m_new == -INFINITY) continue;
-      const float alpha = exp2f(m - m_new), w = seen ? exp2f(z - m_new) : 0.f;
-      m = m_new;
-      l = l * alpha + w;
-      for (int i = 0; i < 16; ++i) acc[i] *= alpha;
-      for (int k = 0; k < kTreeKeys; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        if (!__shfl_sync(0xffffffffu, static_cast<int>(seen), k)) continue;
-        for (int i = 0; i < 8; ++i) {
-          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&keys[k][lane * 16 + 2 * i]));
-          acc[2 * i] = fmaf(wk, f.x, acc[2 * i]);
-          acc[2 * i + 1] = fmaf(wk, f.y, acc[2 * i + 1]);
+    } else if (lane == 0) {
+      // ---------------- the other CTA: its P (and the zeroed slots) handed on
+      // to the leader's issuer with one cluster-scope release per block, which
+      // would cost each softmax warp about a microsecond
+      bool ok = true;
+      int g = 0;
+      while (ok && work.next(p, sg)) {
+        for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
+          if (!(ok = mbar_wait(bar(kTreePLocal), g & 1, ab, kErrWaitSoftmax))) break;
+          mbar_arrive_cluster(mapa_shared(bar(kTreePFull), 0));
         }
       }
     }
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  } else {
+    // ---------------- softmax. Quadrant of tensor-memory lanes q, half ch of
+    // its 64 key columns: row (32 q + lane) mod 64, keys 64 (q / 2) + 32 ch ..
+    // + 32 of the block. The four warps of 32 rows meet at a named barrier for
+    // every block, also after a wait has failed (`ok` false: no more waits, no
+    // more work), so that none is left at it.
+    const int quad = warp & 3, ch = (warp - 2) >> 2;
+    const int row = (32 * quad + lane) & 63, lh = quad >> 1, part = 2 * lh + ch;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    float* xchg = reinterpret_cast<float*>(smem + S::XCHG);
+    uint8_t* prow = smem + S::P + lh * S::CHUNK + row * 128;
+    const float c = p.scale_log2;
+    bool ok = true;
+    int g = 0, tails = 0, turn = 0;
+    // The four threads' values of this row.
+    auto exchange = [&](float v, float (&all)[4]) {
+      float* x = xchg + (turn & 1) * 256;
+      ++turn;
+      x[part * 64 + row] = v;
+      named_barrier(1 + (quad & 1), 128);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) all[i] = x[i * 64 + row];
+    };
+    while (work.next(p, sg)) {
+      const int r = sg.tile * kTreeRows + 64 * rank + row;  // row of the sequence: node * H + head
+      const int live = sg.nodes * p.H;
+      const bool has_tail = static_cast<int64_t>(sg.j1) * kTreeBlock > sg.len;
+      const uint64_t sees = has_tail ? tree_ancestors(p, sg.b, min(r / p.H, kTreeMax)) : 0ull;
+      const int total = sg.len + sg.nodes;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = sg.j0; j < sg.j1; ++j, ++g) {
+        if (ok) ok = warp_wait(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma);
+        tc_fence_after();
+        float x[32];
+        tmem_ld32(tl + kTreeColS + 64u * (g & 1) + 32u * ch, *reinterpret_cast<uint32_t(*)[32]>(x));
+        const int64_t t0 = static_cast<int64_t>(j) * kTreeBlock;
+        const bool tail = t0 + kTreeBlock > sg.len;
+        if (tail) {
+          const uint32_t keep = tree_keep(t0 + 64 * lh + 32 * ch, sg.len, sees);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = (keep >> i) & 1 ? x[i] : -INFINITY;
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = max3(x[i], x[4 + i], x[8 + i]);
+#pragma unroll
+        for (int k0 = 12; k0 < 28; k0 += 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], x[k0 + i], x[k0 + 4 + i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], x[28 + i]);
+        float all[4];
+        exchange(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), all);
+        // Lazy rescaling: the running maximum moves only when a block exceeds
+        // it by more than 8 (in log2), so P < 2^8 and O is rarely touched.
+        const float m_new = fmaxf(m_run, fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3])) * c);
+        const bool resc = (m_new - m_run) > 8.f;
+        float alpha = 1.f;
+        if (resc) {
+          alpha = ex2_approx(m_run - m_new);
+          m_run = m_new;
+        }
+        const float nb = (m_run == -INFINITY) ? 0.f : -m_run;
+        float sm[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          fma2_scalar(x[2 * i], x[2 * i + 1], c, nb);
+          const float p0 = ex2_approx(x[2 * i]);
+          const float p1 = ex2_approx(x[2 * i + 1]);
+          add2(sm[2 * (i & 1)], sm[2 * (i & 1) + 1], p0, p1);
+          pk[i] = pack_bf16x2(p0, p1);
+        }
+        l_run = l_run * alpha + ((sm[0] + sm[1]) + (sm[2] + sm[3]));
+        // P.V of the block before must be done before P is overwritten and O rescaled.
+        if (g > 0 && ok) ok = warp_wait(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma);
+        if (ok && j > sg.j0 && __any_sync(0xffffffffu, resc)) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            uint32_t o[32];
+            tmem_ld32(tl + 128u * ch + c0, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(tl + 128u * ch + c0, o);
+          }
+        }
+        if (ok) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(prow + (((4 * ch + i) ^ (row & 7)) << 4)) =
+                make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        }
+        if (tail) {
+          // Rows of the slots from the first drafted key on: those behind the
+          // last position hold whatever the page held before, and 0 * NaN is
+          // NaN, so they are zeroed; so is what is not finite in a drafted
+          // key's values (a row that sees it gets its NaN from the score).
+          if (ok) ok = warp_wait(bar(kTreeTail), tails & 1, ab, kErrWaitTma);
+          ++tails;
+          if (ok) {
+            const int who = static_cast<int>(threadIdx.x) - 64;  // 256 threads: piece who % 32 of key who / 32
+            const int piece = who & 31, h = piece >> 4, side = (piece >> 3) & 1;
+            for (int k = static_cast<int>(max(int64_t(0), sg.len - t0)) + (who >> 5); k < kTreeBlock; k += 8) {
+              uint4* at = reinterpret_cast<uint4*>(smem + S::RING + ((2 * g + h) % S::UNITS) * S::UNIT +
+                                                   (2 * (k >> 6) + side) * S::CHUNK + (k & 63) * 128 + (piece & 7) * 16);
+              uint4 v = *at;
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (t0 + k >= total) {
+                  w[i] = 0u;
+                } else {
+                  if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+                  if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0x0000ffffu;
+                }
+              }
+              *at = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar(rank == 0 ? kTreePFull : kTreePLocal));
+      }
+      // ---------------- the run's result: o_lat, or its part of it
+      float all[4];
+      exchange(l_run, all);
+      if (ok) ok = warp_wait(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma);
+      if (!ok) continue;
+      tc_fence_after();
+      const float l = (all[0] + all[1]) + (all[2] + all[3]);
+      const int v0 = 256 * ch + 128 * lh;  // this thread's 128 of the 512 values
+      if (sg.j1 - sg.j0 == sg.blocks) {
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        uint4* dst = reinterpret_cast<uint4*>(p.olat + ((static_cast<int64_t>(sg.b) * p.N) * p.H + r) * 512 + v0);
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(tl + 128u * ch + c0, o);
+          if (r < live) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[c0 / 8 + i] =
+                  make_uint4(pack_bf16x2(__uint_as_float(o[8 * i + 0]) * inv, __uint_as_float(o[8 * i + 1]) * inv),
+                             pack_bf16x2(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv),
+                             pack_bf16x2(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv),
+                             pack_bf16x2(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv));
+          }
+        }
+      } else {
+        const int slot = 2 * pair + (sg.first ? 0 : 1);
+        const int tr = 64 * rank + row;
+        float* dst = p.part_o + static_cast<int64_t>(slot) * kTreeSlotFloats + (v0 / 4 * kTreeRows + tr) * 4;
+        if (part == 0) p.part_ml[slot * kTreeRows + tr] = make_float2(m_run, l);
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(tl + 128u * ch + c0, o);
+          if (r < live) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(dst + (c0 / 4 + i) * kTreeRows * 4) =
+                  make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                              __uint_as_float(o[4 * i + 3]));
+          }
+        }
+      }
+    }
   }
-  if (h >= p.H) return;
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.olat + qrow * 512 + lane * 16);
-  for (int i = 0; i < 8; ++i) dst[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the leader's UMMAs read the other CTA's shared memory until here
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// Joins the tiles that several pairs shared, and zeroes the rows of nodes that
+// are not there. Thread: one row of a tile, 16 of its values; with M the
+// largest of the parts' maxima, o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p
+// over the pairs p whose shares meet the tile, in their order.
+constexpr int kTreeJoinThreads = 256;
+constexpr int kTreeJoinBlocks = kTreeRows * 32 / kTreeJoinThreads;  // per tile
+
+__global__ void __launch_bounds__(kTreeJoinThreads)
+tree_combine_kernel(const TreeParams p, int pairs) {
+  const int all_tiles = (p.N * p.H + kTreeRows - 1) / kTreeRows;
+  const int at = static_cast<int>(blockIdx.x) / kTreeJoinBlocks, b = at / all_tiles, tile = at % all_tiles;
+  const int item = static_cast<int>(blockIdx.x) % kTreeJoinBlocks * kTreeJoinThreads + static_cast<int>(threadIdx.x);
+  const int tr = item & 127, v0 = (item >> 7) * 16;
+  const int r = tile * kTreeRows + tr;
+  if (r >= p.N * p.H) return;
+  int len, nodes, tiles, blocks;
+  tree_lengths(p, b, len, nodes);
+  tree_extent(p, len, nodes, tiles, blocks);
+  uint4* dst = reinterpret_cast<uint4*>(p.olat + ((static_cast<int64_t>(b) * p.N) * p.H + r) * 512 + v0);
+  if (r >= nodes * p.H) {
+    dst[0] = dst[1] = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  const int64_t units = p.ustart[p.B], lo = p.ustart[b] + static_cast<int64_t>(tile) * blocks, hi = lo + blocks;
+  int c0 = static_cast<int>(lo * pairs / units);
+  while (tree_share(units, c0 + 1, pairs) <= lo) ++c0;
+  if (tree_share(units, c0 + 1, pairs) >= hi) return;  // one pair's alone
+  float M = -INFINITY;
+  for (int c = c0; c < pairs && tree_share(units, c, pairs) < hi; ++c) {
+    const int64_t s = tree_share(units, c, pairs);
+    if (tree_share(units, c + 1, pairs) > s) M = fmaxf(M, p.part_ml[(2 * c + (s >= lo ? 0 : 1)) * kTreeRows + tr].x);
+  }
+  float acc[16], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int c = c0; c < pairs && tree_share(units, c, pairs) < hi; ++c) {
+    const int64_t s = tree_share(units, c, pairs);
+    if (tree_share(units, c + 1, pairs) <= s) continue;
+    const int slot = 2 * c + (s >= lo ? 0 : 1);
+    const float2 ml = p.part_ml[slot * kTreeRows + tr];
+    if (ml.y == 0.f) continue;  // saw none of its keys
+    const float w = ex2_approx(ml.x - M);
+    sum = fmaf(w, ml.y, sum);
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(slot) * kTreeSlotFloats) +
+                        v0 / 4 * kTreeRows + tr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = src[i * kTreeRows];
+      acc[4 * i] = fmaf(w, v.x, acc[4 * i]);
+      acc[4 * i + 1] = fmaf(w, v.y, acc[4 * i + 1]);
+      acc[4 * i + 2] = fmaf(w, v.z, acc[4 * i + 2]);
+      acc[4 * i + 3] = fmaf(w, v.w, acc[4 * i + 3]);
+    }
+  }
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    dst[i] = make_uint4(pack_bf16x2(acc[8 * i] * inv, acc[8 * i + 1] * inv),
+                        pack_bf16x2(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv),
+                        pack_bf16x2(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv),
+                        pack_bf16x2(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
 }
 
 }  // namespace mla

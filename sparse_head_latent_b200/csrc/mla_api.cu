@@ -66,6 +66,7 @@ struct DeviceState {
   int pairs_wo_narrow = 0;
   int pairs8_kvb = 0;  // CTA pairs of the e4m3 GEMMs
   int pairs8_wo = 0;
+  int pairs_tree = 0;  // CTA pairs of the tree attention
   int* err = nullptr;  // address of g_mla_device_error on this device
 };
 
@@ -164,6 +165,13 @@ int device_state(DeviceState** out) {
                                       GemmM128Unabs::SMEM_BYTES) == cudaSuccess;
       ok = ok && cudaFuncSetAttribute(mla::absorbed_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       mla::AbsSmem::BYTES) == cudaSuccess;
+      ok = ok && cudaFuncSetAttribute(mla::tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      mla::TreeSmem::BYTES) == cudaSuccess;
+      if (ok) {
+        st.pairs_tree = max_pairs(mla::tree_attn_kernel, mla::TreeSmem::BYTES, mla::kTreeThreads);
+        if (st.pairs_tree > mla::kTreeMaxPairs) st.pairs_tree = mla::kTreeMaxPairs;
+        ok = st.pairs_tree > 0;
+      }
       ok = ok && cudaFuncSetAttribute(mla::sparse_mla_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       mla::AttnSmem::BYTES) == cudaSuccess;
       ok = ok && cudaFuncSetAttribute(mla::topk_bitmap_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -273,6 +281,7 @@ struct WsLayout {
   size_t attn8 = kNone, attn8_s = kNone;  // e4m3 activations: quantized attention rows and scales
   int parts = 1;                          // decode: CTAs per (sequence, 64-head group)
   size_t wo_part = kNone;                 // decode: stream-K partial tiles of the output projection
+  size_t tree_start = kNone, tree_ml = kNone, tree_o = kNone;  // tree decode: unit starts, partial tiles
   size_t wo_split = kNone;                // prefill: partial tiles of the output projection's K-split last wave
   int g_abs = 0;       // first tile group on the absorbed path (groups of 4 x 128 query rows)
   int abs_chunk = 0;   // absorbed rows processed per pass
@@ -404,6 +413,9 @@ WsLayout ws_layout(const mla_dims& d, int entry, bool has_topk) {
     w.qabs = take(rows * H * kL * 2);
     w.olat = take(rows * H * kL * 2);
     w.attn = take(rows * H * kDv * 2);
+    w.tree_start = take((static_cast<size_t>(d.B) + 1) * 8);
+    w.tree_ml = take(size_t(2) * mla::kTreeMaxPairs * mla::kTreeRows * 8);
+    w.tree_o = take(size_t(2) * mla::kTreeMaxPairs * mla::kTreeSlotFloats * 4);
     if (rows <= kFewRows) {
       const int bm = rows <= 64 ? 64 : 128;
       const size_t tiles = (rows + bm - 1) / bm * (kD / 128);
@@ -1052,6 +1064,7 @@ int run_decode(const DeviceState* ds, const mla_dims& d, const WsLayout& lay, vo
 // ------------------------------------------------------------------ paged serving
 
 constexpr int64_t kMaxCacheRows = int64_t(1) << 30;  // rows of one layer's cache, positions of one table row
+constexpr int64_t kMaxQueryRows = int64_t(1) << 27;   // (node, head) rows of one call: 32-bit coordinates and grids
 constexpr int kMaxLayers = 65535;                    // a grid dimension
 
 int check_pages(const mla_pages* pg, bool table) {
@@ -1078,6 +1091,60 @@ mla::RopeTable rope_table(const mla_rope_table& t) {
   return r;
 }
 
+// Attention of B trees of N nodes over the pages: q_abs (in the workspace) and
+// q's rotary part against the cache, into o_lat (in the workspace).
+int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pages& pg, const WsLayout& lay, void* ws,
+                          const void* q, const void* kv, const void* pe, const int32_t* table,
+                          const int32_t* cache_len, const int32_t* n_nodes, const int32_t* parents, float scale,
+                          cudaStream_t st) {
+  mla::TreeParams p;
+  p.B = d.B;
+  p.N = d.T;
+  p.H = d.H;
+  p.num_pages = pg.num_pages;
+  p.page_shift = log2_of(pg.page_size);
+  p.table_width = pg.table_width;
+  p.box_shift = p.page_shift < 6 ? p.page_shift : 6;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.table = table;
+  p.cache_len = cache_len;
+  p.n_nodes = n_nodes;
+  p.parents = parents;
+  p.olat = reinterpret_cast<__nv_bfloat16*>(ws_at(ws, lay.olat));
+  p.ustart = reinterpret_cast<int64_t*>(ws_at(ws, lay.tree_start));
+  p.part_o = reinterpret_cast<float*>(ws_at(ws, lay.tree_o));
+  p.part_ml = reinterpret_cast<float2*>(ws_at(ws, lay.tree_ml));
+  p.err = ds->err;
+  const uint64_t qrows = static_cast<uint64_t>(d.B) * d.T * d.H, crows = static_cast<uint64_t>(pg.num_pages) * pg.page_size;
+  const uint32_t box = 1u << p.box_shift;
+  CUtensorMap tkv, tpe, tqa, tq;
+  if (!map_2d(&tkv, kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kL, crows, kL * 2, 64, box) ||
+      !map_2d(&tpe, pe, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDr, crows, kDr * 2, 64, box) ||
+      !map_2d(&tqa, ws_at(ws, lay.qabs), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kL, qrows, kL * 2, 64, 64) ||
+      !map_2d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDn + kDr, qrows, (kDn + kDr) * 2, 64, 64))
+    return MLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * ds->pairs_tree), 1, 1);
+  cfg.blockDim = dim3(mla::kTreeThreads, 1, 1);
+  cfg.dynamicSmemBytes = mla::TreeSmem::BYTES;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t le = cudaSuccess;
+  int rc = timed_launch(7, st, [&] { le = cudaLaunchKernelEx(&cfg, mla::tree_attn_kernel, tkv, tpe, tqa, tq, p); });
+  if (le != cudaSuccess) return MLA_ERR_CUDA;
+  if (rc != MLA_OK) return rc;
+  const int64_t join = static_cast<int64_t>(d.B) * ((d.T * d.H + mla::kTreeRows - 1) / mla::kTreeRows) * mla::kTreeJoinBlocks;
+  return timed_launch(7, st, [&] {
+    mla::tree_combine_kernel<<<static_cast<unsigned>(join), mla::kTreeJoinThreads, 0, st>>>(p, ds->pairs_tree);
+  });
+}
+
 // One decoding step of B trees of N nodes.
 int run_tree_decode(const DeviceState* ds, const mla_dims& d, const mla_pages& pg, const WsLayout& lay, void* ws,
                     const void* q, const void* kv, const void* pe, const int32_t* table, const int32_t* cache_len,
@@ -1095,28 +1162,9 @@ int run_tree_decode(const DeviceState* ds, const mla_dims& d, const mla_pages& p
   void* olat = ws_at(ws, lay.olat);
   void* attn = ws_at(ws, lay.attn);
   if ((rc = launch_gemm_absorb(ds, d.H, rows, q, wk, qabs, st)) != MLA_OK) return rc;
-  mla::TreeParams p;
-  p.B = d.B;
-  p.N = d.T;
-  p.H = d.H;
-  p.num_pages = pg.num_pages;
-  p.page_shift = log2_of(pg.page_size);
-  p.table_width = pg.table_width;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.table = table;
-  p.cache_len = cache_len;
-  p.n_nodes = n_nodes;
-  p.parents = parents;
-  p.qabs = static_cast<const __nv_bfloat16*>(qabs);
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.kv = static_cast<const __nv_bfloat16*>(kv);
-  p.pe = static_cast<const __nv_bfloat16*>(pe);
-  p.olat = static_cast<__nv_bfloat16*>(olat);
-  p.err = ds->err;
-  rc = timed_launch(7, st, [&] {
-    mla::tree_attn_kernel<<<rows * ((d.H + mla::kTreeWarps - 1) / mla::kTreeWarps), 32 * mla::kTreeWarps, 0, st>>>(p);
-  });
-  if (rc != MLA_OK) return rc;
+  if ((rc = launch_tree_attention(ds, d, pg, lay, ws, q, kv, pe, table, cache_len, n_nodes, parents, scale, st)) !=
+      MLA_OK)
+    return rc;
   if ((rc = launch_gemm_unabsorb(ds, d.H, rows, olat, wk, attn, st)) != MLA_OK) return rc;
   const void* wo = W_o;
   if (d.wdtype == MLA_W_E4M3_BLOCK128) {
@@ -1138,7 +1186,9 @@ extern "C" {
 size_t mla_workspace_bytes(const mla_dims* dims, int entry, int has_topk) {
   if (check_dims(dims) != MLA_OK || entry < MLA_ENTRY_KV_UPPROJECT || entry > MLA_ENTRY_TREE_DECODE) return 0;
   if ((entry == MLA_ENTRY_DECODE || entry == MLA_ENTRY_TREE_DECODE) && dims->act != MLA_ACT_BF16) return 0;
-  if (entry == MLA_ENTRY_TREE_DECODE && dims->T > MLA_MAX_TREE) return 0;
+  if (entry == MLA_ENTRY_TREE_DECODE &&
+      (dims->T > MLA_MAX_TREE || static_cast<int64_t>(dims->B) * dims->T * dims->H > kMaxQueryRows))
+    return 0;
   return ws_layout(*dims, entry, has_topk != 0).total;
 }
 
@@ -1410,6 +1460,7 @@ int mla_tree_decode(const mla_dims* dims, const mla_pages* pages, const void* q,
   if (rc != MLA_OK) return rc;
   if (dims->T > MLA_MAX_TREE) return MLA_ERR_SHAPE;
   if (static_cast<int64_t>(dims->B) * dims->T == 0) return MLA_OK;
+  if (static_cast<int64_t>(dims->B) * dims->T * dims->H > kMaxQueryRows) return MLA_ERR_SHAPE;
   if ((rc = check_pages(pages, true)) != MLA_OK) return rc;
   if (pages->layers != 1 || pages->num_pages < 1) return MLA_ERR_SHAPE;
   if (!q || !kv_cache || !k_pe_cache || !block_table || !cache_len || !W_kvb || !W_o || !out ||
