@@ -22,19 +22,18 @@
 // rows 0..63, lanes 64..127 columns [N/2, N). O (64 rows x 512 fp32) then takes
 // 256 of the 512 columns, where 128 rows in one CTA would take all of them
 // and leave none for S. Measured rates of the tensor core alone (clk per block
-// of 128 keys; full rate in brackets): P.V 1050 (1024); Q.K^T 1877 (1152) with
-// Q from shared memory; both together 2600 (2176).
+// of 128 keys; full rate in brackets): P.V 1050 (1024); Q.K^T 1745 (1152), about
+// 47 clk per instruction whatever its N up to 128, the same with Q in tensor
+// memory; both one after the other 2490 (2176).
 //
 // Shared memory per CTA: P (64 rows x 128 keys), Q, a rope slot and a ring of
-// units of four [64 keys x 64] slots. For Q.K^T a CTA holds its own 64 of the
-// block's keys, all 576 values of each; for P.V all 128 keys, its own 128 of
-// each 256 values. The two meet in place: unit h (values [256 h, 256 h + 256))
-// holds the own keys' four 64-value chunks; once Q.K^T has read it, the two
-// slots with values the CTA does not need are loaded again with the other
-// keys' chunks it does need (CTA 0: slots 2, 3 from the other 64 keys; CTA 1:
-// slots 0, 1). So slots 0, 1 always hold keys 0..63 and slots 2, 3 keys
-// 64..127 for P.V in both CTAs, and a key's row crosses L2 -> SM 13/9 times
-// instead of 17/9.
+// eight 16 KB stages that the tensor core empties in the order it is filled:
+// for Q.K^T(j + 1) four stages with the CTA's own 64 keys, 128 of their values
+// each, then for P.V(j) four with 64 keys' 128 values of the CTA's half of the
+// 256. A key's row thus crosses L2 -> SM twice (17 chunks of 64 values per CTA
+// and block). Keeping a block's keys in place for P.V (13 chunks) was built
+// first: its stages stay taken through the softmax, so that next to nothing is
+// prefetched, and a block took 3.4 us instead of MEASURED_US.
 //
 // Roles (320 threads per CTA): warp 0 producer; warp 1 issues the UMMAs
 // (leader) or forwards "P is written" (the other CTA); warps 2..9 softmax: four
@@ -124,11 +123,11 @@ __host__ __device__ __forceinline__ int64_t tree_share(int64_t units, int pair, 
 
 struct TreeSmem {
   static constexpr int CHUNK = 8192;               // [64 keys or rows x 64] bf16
-  static constexpr int UNIT = 4 * CHUNK;
-  static constexpr int UNITS = 4;
+  static constexpr int STAGE = 2 * CHUNK;
+  static constexpr int STAGES = 8;
   static constexpr int Q_CHUNKS = 9;
   static constexpr int RING = 0;
-  static constexpr int ROPE = RING + UNITS * UNIT;
+  static constexpr int ROPE = RING + STAGES * STAGE;
   static constexpr int Q = ROPE + CHUNK;
   static constexpr int P = Q + Q_CHUNKS * CHUNK;   // two [64 rows x 64 keys] chunks
   static constexpr int XCHG = P + 2 * CHUNK;       // [2][4][64] floats
@@ -139,16 +138,15 @@ static_assert(TreeSmem::BYTES <= 232448, "shared memory per CTA");
 
 // Barriers; (L): only the leader's copy is used, by both CTAs.
 enum : int {
-  kTreeKFull = 0,                             // (L) per unit: the own keys' chunks landed in both CTAs
-  kTreeVFull = kTreeKFull + TreeSmem::UNITS,  // (L) per unit: the other keys' chunks landed in both CTAs
-  kTreeEmpty = kTreeVFull + TreeSmem::UNITS,  // per unit: the P.V that read it is done
-  kTreeSFull = kTreeEmpty + TreeSmem::UNITS,  // per S buffer: Q.K^T of a block is done
+  kTreeFull = 0,                               // (L) per stage: landed in both CTAs
+  kTreeEmpty = kTreeFull + TreeSmem::STAGES,   // per stage: the products that read it are done
+  kTreeSFull = kTreeEmpty + TreeSmem::STAGES,  // per S buffer: Q.K^T of a block is done
   kTreePVDone = kTreeSFull + 2,               // P.V of a block is done
   kTreeRopeFull,                              // (L) the rope slot landed in both CTAs
   kTreeQFull,                                 // (L) Q landed in both CTAs
   kTreePLocal,                                // (the other CTA) its eight warps have written P
   kTreePFull,                                 // (L) P of both CTAs is written
-  kTreeTail,                                  // the other keys' chunks of a block with drafted keys landed in this CTA
+  kTreeTail,                                  // the values of a block with drafted keys landed in this CTA
   kTreeDrain,
   kTreeBars
 };
@@ -302,55 +300,71 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
   TreeSeg sg = {};
 
   if (warp == 0) {
-    // ---------------- producer: the whole warp, each lane at most one box at a time
-    const int boxes = 64 >> p.box_shift;  // per 64 keys
+    // ---------------- producer: the whole warp, each lane at most one box of a
+    // stage. It has about 250 clk per stage, so what a stage needs is computed
+    // once here, and table entries are fetched two blocks before their use.
+    const int box_log = 6 - p.box_shift;  // boxes per 64 keys, log2
+    const int bx = lane & ((1 << box_log) - 1), chunk = lane >> box_log;
+    const bool loads = chunk < 2;
     const int cache_rows = p.num_pages << p.page_shift;
-    const uint32_t ring = smem_u32(smem + S::RING);
+    const uint32_t dst0 = smem_u32(smem + S::RING) + chunk * S::CHUNK + (bx << (p.box_shift + 7));
+    const uint32_t full0 = bar(kTreeFull), full0_leader = mapa_shared(full0, 0), empty0 = bar(kTreeEmpty);
+    const int page_mask = (1 << p.page_shift) - 1;
     bool ok = true;
-    int g = 0;
-    // Cache row of box `lane` (of 2 * boxes) of block j; a box behind the last
-    // position reads zeros from behind the cache.
-    auto rows_of = [&](int j) -> int {
+    int g = 0;           // blocks so far
+    uint32_t quads = 0;  // runs of four stages so far
+    // Table entry of box `lane` (of a block's 128 keys) of block j; -1 behind the last position.
+    auto entry_of = [&](int j) -> int {
       const int64_t t = static_cast<int64_t>(j) * kTreeBlock + (static_cast<int64_t>(lane) << p.box_shift);
-      if (lane >= 2 * boxes || j >= sg.blocks || t >= sg.len + sg.nodes) return cache_rows;
-      const int page = __ldg(p.table + static_cast<int64_t>(sg.b) * p.table_width + (t >> p.page_shift));
-      if (page < 0 || page >= p.num_pages) {
-        atomicCAS(p.err, 0, kErrPage);
+      if (lane >= (2 << box_log) || j >= sg.j1 || t >= sg.len + sg.nodes) return -1;
+      const int e = __ldg(p.table + static_cast<int64_t>(sg.b) * p.table_width + (t >> p.page_shift));
+      return e < 0 ? INT32_MIN : e;  // -1 is ours
+    };
+    // Its cache row; nothing to read: a row behind the cache, which loads zeros.
+    auto row_of = [&](int j, int entry) -> int {
+      if (entry < 0 || entry >= p.num_pages) {
+        if (entry != -1) atomicCAS(p.err, 0, kErrPage);
         return cache_rows;
       }
-      return (page << p.page_shift) + static_cast<int>(t & ((int64_t(1) << p.page_shift) - 1));
+      return (entry << p.page_shift) + ((j * kTreeBlock + (lane << p.box_shift)) & page_mask);
     };
-    // Loads four chunks' boxes of keys half `half` into slots slot0 .. : lane
-    // = chunk * boxes + box.
-    auto load_half = [&](int rows, int half, int chunk0, int chunks, uint32_t dst, uint32_t barrier, bool local) {
-      const int c = lane / boxes, x = lane % boxes;
-      const int row = __shfl_sync(0xffffffffu, rows, half * boxes + x);
-      if (c < chunks) {
-        const uint32_t d = dst + c * S::CHUNK + ((x << p.box_shift) << 7);
-        if (local)
-          tma_load_2d(d, &tm_kv, barrier, (chunk0 + c) * 64, row);
-        else
-          tma_load_2d_pair(d, &tm_kv, barrier, (chunk0 + c) * 64, row);
-      }
-    };
-    auto load_keys = [&](int block, int rows) -> bool {  // block: running index over the pair's blocks
-      for (int h = 0; h < 2; ++h) {
-        const int u = 2 * block + h, s = u % S::UNITS;
-        if (!warp_wait(bar(kTreeEmpty + s), ((u / S::UNITS) & 1) ^ 1, ab, kErrWaitConsumer)) return false;
-        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(kTreeKFull + s), 2 * S::UNIT);
+    // Four stages: two chunks of 64 keys each, from chunk columns c0, c1, c2, c3
+    // and the rows (per lane) ra for stages 0 and 2, rb for 1 and 3. With
+    // `local` the bytes count on this CTA's kTreeTail, and "P is written" tells
+    // the issuer that they have landed.
+    auto load_quad = [&](int ra, int rb, int c0, int c1, int c2, int c3, bool local) -> bool {
+      const uint32_t s0 = (quads & 1) * 4, parity = ((quads >> 1) & 1) ^ 1;
+      ++quads;
+      const int cs[4] = {c0, c1, c2, c3};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t s = s0 + i;
+        if (!warp_wait_all(empty0 + 8 * s, parity, ab, kErrWaitConsumer)) return false;
+        if (rank == 0 && lane == 0) {
+          if (local)
+            mbar_arrive(full0 + 8 * s);
+          else
+            mbar_arrive_expect_tx(full0 + 8 * s, 2 * S::STAGE);
+        }
         __syncwarp();
-        load_half(rows, rank, 4 * h, 4, ring + s * S::UNIT, mapa_shared(bar(kTreeKFull + s), 0), false);
+        if (loads) {
+          const int col = (cs[i] + chunk) * 64, row = (i & 1) ? rb : ra;
+          if (local)
+            tma_load_2d(dst0 + s * S::STAGE, &tm_kv, bar(kTreeTail), col, row);
+          else
+            tma_load_2d_pair(dst0 + s * S::STAGE, &tm_kv, full0_leader + 8 * s, col, row);
+        }
       }
       return true;
     };
-    auto load_rope = [&](int rows) {
+    auto load_rope = [&](int own) {
       if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(kTreeRopeFull), 2 * S::CHUNK);
       __syncwarp();
-      const int row = __shfl_sync(0xffffffffu, rows, rank * boxes + lane % boxes);
-      if (lane < boxes)
-        tma_load_2d_pair(smem_u32(smem + S::ROPE) + ((lane << p.box_shift) << 7), &tm_pe,
-                         mapa_shared(bar(kTreeRopeFull), 0), 0, row);
+      if (chunk == 0)
+        tma_load_2d_pair(smem_u32(smem + S::ROPE) + (bx << (p.box_shift + 7)), &tm_pe,
+                         mapa_shared(bar(kTreeRopeFull), 0), 0, own);
     };
+    const int own_lane = (rank << box_log) + bx, first_lane = bx, second_lane = (1 << box_log) + bx;
     while (ok && work.next(p, sg)) {
       // Q: rows of this tile; those past the sequence's last belong to another
       // sequence or to none, and are not stored. The previous run's products
@@ -365,42 +379,33 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         else
           tma_load_2d_pair(d, &tm_q, qb, 128, qrow);
       }
-      const int n = sg.j1 - sg.j0;
-      int r0 = rows_of(sg.j0), r1 = rows_of(sg.j0 + 1), r2 = rows_of(sg.j0 + 2);
-      ok = load_keys(g, r0);
-      if (ok) load_rope(r0);
-      if (ok && n > 1) ok = load_keys(g + 1, r1);
-      for (int j = 0; ok && j < n; ++j) {
-        const int r3 = j + 3 < n ? rows_of(sg.j0 + j + 3) : cache_rows;
-        const int block = g + j;
-        if (!(ok = warp_wait(bar(kTreeSFull + (block & 1)), (block >> 1) & 1, ab, kErrWaitMma))) break;
-        // The other keys' chunks, over the two slots of each unit this CTA is done with.
-        const bool tail = static_cast<int64_t>(sg.j0 + j + 1) * kTreeBlock > sg.len;
-        if (tail && lane == 0) mbar_arrive_expect_tx(bar(kTreeTail), 4 * S::CHUNK);
-        for (int h = 0; h < 2; ++h) {
-          const int u = 2 * block + h, s = u % S::UNITS;
-          if (rank == 0 && lane == 0) {
-            if (tail)
-              mbar_arrive(bar(kTreeVFull + s));  // "P is written" then tells that they landed, too
-            else
-              mbar_arrive_expect_tx(bar(kTreeVFull + s), 4 * S::CHUNK);
-          }
-          __syncwarp();
-          load_half(r0, 1 - rank, 4 * h + 2 * rank, 2, ring + s * S::UNIT + (rank == 0 ? 2 * S::CHUNK : 0),
-                    tail ? bar(kTreeTail) : mapa_shared(bar(kTreeVFull + s), 0), tail);
-        }
-        if (j + 1 < n) load_rope(r1);
-        if (j + 2 < n) ok = load_keys(block + 2, r2);
+      int e1 = entry_of(sg.j0 + 1), e2 = entry_of(sg.j0 + 2);
+      int r0 = row_of(sg.j0, entry_of(sg.j0));
+      int own = __shfl_sync(0xffffffffu, r0, own_lane);
+      ok = load_quad(own, own, 0, 2, 4, 6, false);
+      if (ok) load_rope(own);
+      for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
+        const int r1 = row_of(j + 1, e1);
+        e1 = e2;
+        e2 = entry_of(j + 3);
+        const int ra = __shfl_sync(0xffffffffu, r0, first_lane), rb = __shfl_sync(0xffffffffu, r0, second_lane);
+        own = __shfl_sync(0xffffffffu, r1, own_lane);
+        if (j + 1 < sg.j1) ok = load_quad(own, own, 0, 2, 4, 6, false);
+        // Q.K^T(j) is done: the rope slot is free, and after the last block Q.
+        if (ok) ok = warp_wait_all(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma);
+        if (ok && j + 1 < sg.j1) load_rope(own);
+        const bool tail = static_cast<int64_t>(j + 1) * kTreeBlock > sg.len;
+        if (ok && tail && lane == 0) mbar_arrive_expect_tx(bar(kTreeTail), 4 * S::STAGE);
+        if (ok) ok = load_quad(ra, rb, 2 * rank, 2 * rank, 4 + 2 * rank, 4 + 2 * rank, tail);
         r0 = r1;
-        r1 = r2;
-        r2 = r3;
       }
-      g += n;
     }
     if (!ok) spin_ns(2000000);  // let issued loads land before the CTA can exit
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      // ---------------- UMMA issuer: Q.K^T of block j + 1, then P.V of block j
+    if (rank == 0) {
+      // ---------------- UMMA issuer, the whole warp (see umma_ss_pair_x4; each
+      // lane waits for itself, and only the issuing lane's outcome counts):
+      // Q.K^T of block j + 1, then P.V of block j
       constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 256, 0, 1);
       const uint64_t dring = smem_desc_sw128(smem_u32(smem + S::RING), 16, 1024);
@@ -408,44 +413,45 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       const uint64_t drope = smem_desc_sw128(smem_u32(smem + S::ROPE), 16, 1024);
       const uint64_t dq = smem_desc_sw128(smem_u32(smem + S::Q), 16, 1024);
       const uint64_t dp = smem_desc_sw128(smem_u32(smem + S::P), 16, 1024);
+      const uint32_t full0 = bar(kTreeFull), empty0 = bar(kTreeEmpty), issue = elect_lane();
       bool ok = true;
       int g = 0, seg = 0, commits = 0;
+      uint32_t quads = 0;  // runs of four stages so far
       auto qk = [&](int block) -> bool {
         const uint32_t ts = tmem + kTreeColS + 64u * static_cast<uint32_t>(block & 1);
-        for (int h = 0; h < 2; ++h) {
-          const int u = 2 * block + h, s = u % S::UNITS;
-          if (!mbar_wait(bar(kTreeKFull + s), (u / S::UNITS) & 1, ab, kErrWaitTma)) return false;
-          tc_fence_after();
+        constexpr int kChunk = S::CHUNK >> 4, kStage = S::STAGE >> 4;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t in = ((i >> 2) * S::CHUNK + (i & 3) * 32) >> 4;
-            umma_ss_pair(ts, dq + ((h * S::UNIT) >> 4) + in, dring + ((s * S::UNIT) >> 4) + in, idesc_qk,
-                         (h > 0 || i > 0) ? 1u : 0u);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t s = (quads & 1) * 4 + i;
+          if (!mbar_wait(full0 + 8 * s, (quads >> 1) & 1, ab, kErrWaitTma)) return false;
+          tc_fence_after();
+          const uint64_t k = dring + s * kStage;
+          umma_ss_pair_x4<2, 2>(ts, dq + i * kStage, k, idesc_qk, i > 0 ? 1u : 0u, issue);
+          umma_ss_pair_x4<2, 2>(ts, dq + i * kStage + kChunk, k + kChunk, idesc_qk, 1u, issue);
+          umma_commit_pair_warp(empty0 + 8 * s, 0x3, issue);
         }
+        ++quads;
         if (!mbar_wait(bar(kTreeRopeFull), block & 1, ab, kErrWaitTma)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          umma_ss_pair(ts, dq + ((8 * S::CHUNK + i * 32) >> 4), drope + ((i * 32) >> 4), idesc_qk, 1u);
-        umma_commit_pair(bar(kTreeSFull + (block & 1)), 0x3);
+        umma_ss_pair_x4<2, 2>(ts, dq + 8 * kChunk, drope, idesc_qk, 1u, issue);
+        umma_commit_pair_warp(bar(kTreeSFull + (block & 1)), 0x3, issue);
         ++commits;
         return true;
       };
       auto pv = [&](int block, bool fresh) -> bool {
         if (!mbar_wait_cluster(bar(kTreePFull), block & 1, ab, kErrWaitSoftmax)) return false;
-        for (int h = 0; h < 2; ++h) {
-          const int u = 2 * block + h, s = u % S::UNITS;
-          if (!mbar_wait(bar(kTreeVFull + s), (u / S::UNITS) & 1, ab, kErrWaitTma)) return false;
-          tc_fence_after();
+        constexpr int kChunk = S::CHUNK >> 4, kStage = S::STAGE >> 4;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ss_pair(tmem + 128u * h, dp + (((kk >> 2) * S::CHUNK + (kk & 3) * 32) >> 4),
-                         dring_mn + ((s * S::UNIT + (kk >> 2) * 2 * S::CHUNK + (kk & 3) * 2048) >> 4), idesc_pv,
-                         (!fresh || kk > 0) ? 1u : 0u);
-          umma_commit_pair(bar(kTreeEmpty + s), 0x3);
+        for (int i = 0; i < 4; ++i) {  // values [256 (i / 2), + 256) of keys [64 (i % 2), + 64)
+          const uint32_t s = (quads & 1) * 4 + i;
+          if (!mbar_wait(full0 + 8 * s, (quads >> 1) & 1, ab, kErrWaitTma)) return false;
+          tc_fence_after();
+          umma_ss_pair_x4<2, 128>(tmem + 128u * (i >> 1), dp + (i & 1) * kChunk, dring_mn + s * kStage, idesc_pv,
+                                  (!fresh || (i & 1)) ? 1u : 0u, issue);
+          umma_commit_pair_warp(empty0 + 8 * s, 0x3, issue);
         }
-        umma_commit_pair(bar(kTreePVDone), 0x3);
+        ++quads;
+        umma_commit_pair_warp(bar(kTreePVDone), 0x3, issue);
         ++commits;
         return true;
       };
@@ -462,7 +468,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         ++seg;
       }
       if (!ok && commits > 0) {
-        umma_commit_pair(bar(kTreeDrain), 0x1);
+        umma_commit_pair_warp(bar(kTreeDrain), 0x1, issue);
         mbar_wait_drain(bar(kTreeDrain), 0);
       }
     } else if (lane == 0) {
@@ -491,7 +497,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
     uint8_t* prow = smem + S::P + lh * S::CHUNK + row * 128;
     const float c = p.scale_log2;
     bool ok = true;
-    int g = 0, tails = 0, turn = 0;
+    int g = 0, tails = 0, turn = 0, st = 0;
     // The four threads' values of this row.
     auto exchange = [&](float v, float (&all)[4]) {
       float* x = xchg + (turn & 1) * 256;
@@ -509,7 +515,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       const int total = sg.len + sg.nodes;
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = sg.j0; j < sg.j1; ++j, ++g) {
-        if (ok) ok = warp_wait(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma);
+        if (ok) ok = warp_wait_all(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma);
         tc_fence_after();
         float x[32];
         tmem_ld32(tl + kTreeColS + 64u * (g & 1) + 32u * ch, *reinterpret_cast<uint32_t(*)[32]>(x));
@@ -554,7 +560,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         }
         l_run = l_run * alpha + ((sm[0] + sm[1]) + (sm[2] + sm[3]));
         // P.V of the block before must be done before P is overwritten and O rescaled.
-        if (g > 0 && ok) ok = warp_wait(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma);
+        if (g > 0 && ok) ok = warp_wait_all(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma);
         if (ok && j > sg.j0 && __any_sync(0xffffffffu, resc)) {
           tc_fence_after();
 #pragma unroll 1
@@ -573,18 +579,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
                 make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
         }
         if (tail) {
-          // Rows of the slots from the first drafted key on: those behind the
-          // last position hold whatever the page held before, and 0 * NaN is
+          // The values from the first drafted key on: those behind the last
+          // position hold whatever the page held before, and 0 * NaN is
           // NaN, so they are zeroed; so is what is not finite in a drafted
           // key's values (a row that sees it gets its NaN from the score).
-          if (ok) ok = warp_wait(bar(kTreeTail), tails & 1, ab, kErrWaitTma);
+          if (ok) ok = warp_wait_all(bar(kTreeTail), tails & 1, ab, kErrWaitTma);
           ++tails;
           if (ok) {
             const int who = static_cast<int>(threadIdx.x) - 64;  // 256 threads: piece who % 32 of key who / 32
-            const int piece = who & 31, h = piece >> 4, side = (piece >> 3) & 1;
+            const int piece = who & 31, h = piece >> 4, chunk = (piece >> 3) & 1;
+            // The run's stages: four for its first block's keys, then per block the next one's keys and its values.
+            const int sv = st + 8 * (j - sg.j0) + (j + 1 < sg.j1 ? 8 : 4);
             for (int k = static_cast<int>(max(int64_t(0), sg.len - t0)) + (who >> 5); k < kTreeBlock; k += 8) {
-              uint4* at = reinterpret_cast<uint4*>(smem + S::RING + ((2 * g + h) % S::UNITS) * S::UNIT +
-                                                   (2 * (k >> 6) + side) * S::CHUNK + (k & 63) * 128 + (piece & 7) * 16);
+              uint4* at = reinterpret_cast<uint4*>(smem + S::RING + ((sv + 2 * h + (k >> 6)) & (S::STAGES - 1)) * S::STAGE +
+                                                   chunk * S::CHUNK + (k & 63) * 128 + (piece & 7) * 16);
               uint4 v = *at;
               uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -605,10 +613,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(bar(rank == 0 ? kTreePFull : kTreePLocal));
       }
+      st += 8 * (sg.j1 - sg.j0);
       // ---------------- the run's result: o_lat, or its part of it
       float all[4];
       exchange(l_run, all);
-      if (ok) ok = warp_wait(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma);
+      if (ok) ok = warp_wait_all(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma);
       if (!ok) continue;
       tc_fence_after();
       const float l = (all[0] + all[1]) + (all[2] + all[3]);

@@ -170,6 +170,12 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const A
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// Every lane waits; true if all saw the phase complete (64 clk when it already
+// has, against 155 with one lane waiting and a shuffle).
+__device__ __forceinline__ bool warp_wait_all(uint32_t bar, uint32_t parity, const Abort& ab, int code) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, code)) != 0;
+}
+
 // Bounded wait used while draining after an abort: never records an error.
 __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
@@ -465,6 +471,52 @@ __device__ __forceinline__ void umma_ss_pair(uint32_t d_tmem, uint64_t a_desc, u
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+  return r;
+}
+
+// Four pair UMMAs (K = 64) whose descriptors advance by DA and DB (16-byte
+// units), and umma_commit_pair, written for a whole warp that stays on one
+// path: the lane with `issue` set (elect_lane) issues, the others only keep the
+// descriptors warp-uniform. They then live in uniform registers, where the
+// instruction wants them. Measured for M = 128, N = 128, K = 16 (32 clk each at
+// the full rate), waits on a barrier before every four included: 34 clk per
+// UMMA like this, 52 with a separate statement each, and about 90 issued from an
+// `if (lane == 0)` block, where each operand is moved to a uniform register
+// first.
+template <int DA, int DB>
+__device__ __forceinline__ void umma_ss_pair_x4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate_first, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, t;\n\t"
+      ".reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 a1, %1, %6;\n\tadd.s64 b1, %2, %9;\n\t"
+      "add.s64 a2, %1, %7;\n\tadd.s64 b2, %2, %10;\n\t"
+      "add.s64 a3, %1, %8;\n\tadd.s64 b3, %2, %11;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate_first), "r"(issue), "n"(DA), "n"(2 * DA), "n"(3 * DA),
+      "n"(DB), "n"(2 * DB), "n"(3 * DB)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_pair_warp(uint32_t bar, uint16_t cta_mask, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"(cta_mask), "r"(issue)
       : "memory");
 }
 
