@@ -26,18 +26,23 @@
 // 47 clk per instruction whatever its N up to 128, the same with Q in tensor
 // memory; both one after the other 2490 (2176).
 //
-// Shared memory per CTA: P (64 rows x 128 keys), Q, a rope slot and a ring of
-// eight 16 KB stages that the tensor core empties in the order it is filled:
-// for Q.K^T(j + 1) four stages with the CTA's own 64 keys, 128 of their values
-// each, then for P.V(j) four with 64 keys' 128 values of the CTA's half of the
-// 256. A key's row thus crosses L2 -> SM twice (17 chunks of 64 values per CTA
-// and block). Keeping a block's keys in place for P.V (13 chunks) was built
-// first: its stages stay taken through the softmax, so that next to nothing is
-// prefetched, and a block took 3.4 us instead of MEASURED_US.
+// A block costs 2.2k clk of tensor core but 136 KB per CTA if Q.K^T's keys and
+// P.V's values are loaded apart, and L2 -> SM then sets the pace (a block took
+// 4.1k clk; with half the bytes 2.9k). So a block is kept in place: for Q.K^T a
+// CTA holds its own 64 of the block's keys, all 512 latent values of each, as
+// four 16 KB groups of 128 values; for P.V it needs all 128 keys, its own half
+// of each 256 values. The two meet: group i = 2 h + r of CTA r is already the
+// values [256 h + 128 r, + 128) of its own keys. The other two groups it is done
+// with once Q.K^T has read them, and loads them again with the other keys' values
+// of its half. Group 2 h + k then holds, in both CTAs, keys [64 k, + 64) of the
+// block, values of half h, and each CTA has loaded 13 chunks of 64 values instead
+// of 17. The price is that groups stay taken through the softmax: eleven fit,
+// which is 2.75 blocks, because six of Q's nine chunks live in tensor memory
+// (next to O and one S; Q.K^T(j + 1) waits until S(j) has been loaded, which P.V(j
+// - 1) covers).
 //
-// Roles (320 threads per CTA): warp 0 producer; warp 1 issues the UMMAs
-// (leader) or forwards "P is written" (the other CTA); warps 2..9 softmax: four
-// threads per row, one for each quarter of the block's keys, agree on the
+// Roles (320 threads per CTA): warp 0 producer; warp 1 of the leader issues
+// the UMMAs; warps 2..9 softmax: four threads per row, one for each quarter of the block's keys, agree on the
 // running maximum through shared memory.
 #pragma once
 
@@ -123,11 +128,12 @@ __host__ __device__ __forceinline__ int64_t tree_share(int64_t units, int pair, 
 
 struct TreeSmem {
   static constexpr int CHUNK = 8192;               // [64 keys or rows x 64] bf16
-  static constexpr int STAGE = 2 * CHUNK;
-  static constexpr int STAGES = 8;
-  static constexpr int Q_CHUNKS = 9;
+  static constexpr int GROUP = 2 * CHUNK;
+  static constexpr int GROUPS = 11;
+  static constexpr int Q_TMEM = 6;                 // chunks of Q in tensor memory, the first of the nine
+  static constexpr int Q_CHUNKS = 9 - Q_TMEM;      // and in shared memory
   static constexpr int RING = 0;
-  static constexpr int ROPE = RING + STAGES * STAGE;
+  static constexpr int ROPE = RING + GROUPS * GROUP;
   static constexpr int Q = ROPE + CHUNK;
   static constexpr int P = Q + Q_CHUNKS * CHUNK;   // two [64 rows x 64 keys] chunks
   static constexpr int XCHG = P + 2 * CHUNK;       // [2][4][64] floats
@@ -138,20 +144,24 @@ static_assert(TreeSmem::BYTES <= 232448, "shared memory per CTA");
 
 // Barriers; (L): only the leader's copy is used, by both CTAs.
 enum : int {
-  kTreeFull = 0,                               // (L) per stage: landed in both CTAs
-  kTreeEmpty = kTreeFull + TreeSmem::STAGES,   // per stage: the products that read it are done
-  kTreeSFull = kTreeEmpty + TreeSmem::STAGES,  // per S buffer: Q.K^T of a block is done
-  kTreePVDone = kTreeSFull + 2,               // P.V of a block is done
-  kTreeRopeFull,                              // (L) the rope slot landed in both CTAs
-  kTreeQFull,                                 // (L) Q landed in both CTAs
-  kTreePLocal,                                // (the other CTA) its eight warps have written P
-  kTreePFull,                                 // (L) P of both CTAs is written
-  kTreeTail,                                  // the values of a block with drafted keys landed in this CTA
+  kTreeKFull = 0,                               // (L) per group: the own keys' values landed in both CTAs
+  kTreeVFull = kTreeKFull + TreeSmem::GROUPS,   // (L) per group: the other keys' values landed in the CTA that reloads it
+  kTreeEmpty = kTreeVFull + TreeSmem::GROUPS,   // per group: the P.V that read it is done
+  kTreeSFull = kTreeEmpty + TreeSmem::GROUPS,   // Q.K^T of a block is done
+  kTreeSFree,                                   // (L) S is in the softmax warps' registers (sixteen warps)
+  kTreePVDone,                                  // P.V of a block is done
+  kTreeRopeFull,                                // (L) the rope chunk landed in both CTAs
+  kTreeQFull,                                   // (L) Q's shared-memory part landed in both CTAs
+  kTreeQReady,                                  // (L) its tensor-memory part is written (sixteen warps)
+  kTreePFull,                                   // (L) P of both CTAs is written (sixteen warps)
+  kTreeTail,                                    // the reloaded values of a block with drafted keys landed in this CTA
   kTreeDrain,
   kTreeBars
 };
+static_assert(8 * kTreeBars + 8 <= 384, "barriers, then the share's start at byte 384");
 
-constexpr uint32_t kTreeColS = 256;  // S buffers at 256 and 320; O at 0 and 128
+constexpr uint32_t kTreeColS = 256;  // S; O at 0 and 128
+constexpr uint32_t kTreeColQ = 320;  // Q's first six chunks, 32 columns each
 
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -227,7 +237,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kTreeBars; ++i) mbar_init(bar(i), i == kTreePLocal ? 8 : i == kTreePFull ? 9 : 1);
+    for (int i = 0; i < kTreeBars; ++i) mbar_init(bar(i), i == kTreeSFree || i == kTreePFull || i == kTreeQReady ? 16 : 1);
     *abort_word = 0;
     fence_barrier_init();
   }
@@ -308,11 +318,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
     const bool loads = chunk < 2;
     const int cache_rows = p.num_pages << p.page_shift;
     const uint32_t dst0 = smem_u32(smem + S::RING) + chunk * S::CHUNK + (bx << (p.box_shift + 7));
-    const uint32_t full0 = bar(kTreeFull), full0_leader = mapa_shared(full0, 0), empty0 = bar(kTreeEmpty);
+    const uint32_t kfull0 = bar(kTreeKFull), vfull0 = bar(kTreeVFull), empty0 = bar(kTreeEmpty);
+    const uint32_t kfull0_leader = mapa_shared(kfull0, 0), vfull0_leader = mapa_shared(vfull0, 0);
     const int page_mask = (1 << p.page_shift) - 1;
     bool ok = true;
-    int g = 0;           // blocks so far
-    uint32_t quads = 0;  // runs of four stages so far
+    int g = 0;                    // blocks so far
+    uint32_t ks = 0, parity = 0;  // the next group of keys
+    uint32_t vs = 0;              // the next group of values
     // Table entry of box `lane` (of a block's 128 keys) of block j; -1 behind the last position.
     auto entry_of = [&](int j) -> int {
       const int64_t t = static_cast<int64_t>(j) * kTreeBlock + (static_cast<int64_t>(lane) << p.box_shift);
@@ -328,34 +340,41 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       }
       return (entry << p.page_shift) + ((j * kTreeBlock + (lane << p.box_shift)) & page_mask);
     };
-    // Four stages: two chunks of 64 keys each, from chunk columns c0, c1, c2, c3
-    // and the rows (per lane) ra for stages 0 and 2, rb for 1 and 3. With
-    // `local` the bytes count on this CTA's kTreeTail, and "P is written" tells
-    // the issuer that they have landed.
-    auto load_quad = [&](int ra, int rb, int c0, int c1, int c2, int c3, bool local) -> bool {
-      const uint32_t s0 = (quads & 1) * 4, parity = ((quads >> 1) & 1) ^ 1;
-      ++quads;
-      const int cs[4] = {c0, c1, c2, c3};
+    // A block's own keys, rows `own` (per lane).
+    auto load_keys = [&](int own) -> bool {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t s = s0 + i;
-        if (!warp_wait_all(empty0 + 8 * s, parity, ab, kErrWaitConsumer)) return false;
-        if (rank == 0 && lane == 0) {
-          if (local)
-            mbar_arrive(full0 + 8 * s);
-          else
-            mbar_arrive_expect_tx(full0 + 8 * s, 2 * S::STAGE);
-        }
+        if (!warp_wait_all(empty0 + 8 * ks, parity ^ 1, ab, kErrWaitConsumer)) return false;
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(kfull0 + 8 * ks, 2 * S::GROUP);
         __syncwarp();
-        if (loads) {
-          const int col = (cs[i] + chunk) * 64, row = (i & 1) ? rb : ra;
-          if (local)
-            tma_load_2d(dst0 + s * S::STAGE, &tm_kv, bar(kTreeTail), col, row);
-          else
-            tma_load_2d_pair(dst0 + s * S::STAGE, &tm_kv, full0_leader + 8 * s, col, row);
-        }
+        if (loads) tma_load_2d_pair(dst0 + ks * S::GROUP, &tm_kv, kfull0_leader + 8 * ks, (2 * i + chunk) * 64, own);
+        if (++ks == S::GROUPS) ks = 0, parity ^= 1;
       }
       return true;
+    };
+    // The other keys' values, rows `other`, over the groups this CTA is done
+    // with. With `tail` the bytes count on this CTA's kTreeTail, and "P is
+    // written" tells the issuer that they have landed.
+    auto load_values = [&](int other, bool tail) {
+      if (tail && lane == 0) mbar_arrive_expect_tx(bar(kTreeTail), 2 * S::GROUP);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (rank == 0 && lane == 0) {
+          if (tail)
+            mbar_arrive(vfull0 + 8 * vs);
+          else
+            mbar_arrive_expect_tx(vfull0 + 8 * vs, S::GROUP);
+        }
+        __syncwarp();
+        if (loads && (i & 1) != rank) {
+          const int col = (4 * (i >> 1) + 2 * rank + chunk) * 64;
+          if (tail)
+            tma_load_2d(dst0 + vs * S::GROUP, &tm_kv, bar(kTreeTail), col, other);
+          else
+            tma_load_2d_pair(dst0 + vs * S::GROUP, &tm_kv, vfull0_leader + 8 * vs, col, other);
+        }
+        if (++vs == S::GROUPS) vs = 0;
+      }
     };
     auto load_rope = [&](int own) {
       if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(kTreeRopeFull), 2 * S::CHUNK);
@@ -364,7 +383,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         tma_load_2d_pair(smem_u32(smem + S::ROPE) + (bx << (p.box_shift + 7)), &tm_pe,
                          mapa_shared(bar(kTreeRopeFull), 0), 0, own);
     };
-    const int own_lane = (rank << box_log) + bx, first_lane = bx, second_lane = (1 << box_log) + bx;
+    const int own_lane = (rank << box_log) + bx, other_lane = ((rank ^ 1) << box_log) + bx;
     while (ok && work.next(p, sg)) {
       // Q: rows of this tile; those past the sequence's last belong to another
       // sequence or to none, and are not stored. The previous run's products
@@ -374,30 +393,30 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       if (lane < S::Q_CHUNKS) {
         const int qrow = (sg.b * p.N) * p.H + sg.tile * kTreeRows + 64 * rank;
         const uint32_t d = smem_u32(smem + S::Q) + lane * S::CHUNK, qb = mapa_shared(bar(kTreeQFull), 0);
-        if (lane < 8)
-          tma_load_2d_pair(d, &tm_qabs, qb, lane * 64, qrow);
+        if (lane + S::Q_TMEM < 8)
+          tma_load_2d_pair(d, &tm_qabs, qb, (lane + S::Q_TMEM) * 64, qrow);
         else
           tma_load_2d_pair(d, &tm_q, qb, 128, qrow);
       }
-      int e1 = entry_of(sg.j0 + 1), e2 = entry_of(sg.j0 + 2);
-      int r0 = row_of(sg.j0, entry_of(sg.j0));
+      // r<k>: cache rows (per lane) of block j + k; e3: table entries of block j + 3.
+      const int e1 = entry_of(sg.j0 + 1), e2 = entry_of(sg.j0 + 2);
+      int r0 = row_of(sg.j0, entry_of(sg.j0)), r1 = row_of(sg.j0 + 1, e1), r2 = row_of(sg.j0 + 2, e2);
       int own = __shfl_sync(0xffffffffu, r0, own_lane);
-      ok = load_quad(own, own, 0, 2, 4, 6, false);
+      ok = load_keys(own);
       if (ok) load_rope(own);
+      if (ok && sg.j0 + 1 < sg.j1) ok = load_keys(__shfl_sync(0xffffffffu, r1, own_lane));
       for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
-        const int r1 = row_of(j + 1, e1);
-        e1 = e2;
-        e2 = entry_of(j + 3);
-        const int ra = __shfl_sync(0xffffffffu, r0, first_lane), rb = __shfl_sync(0xffffffffu, r0, second_lane);
-        own = __shfl_sync(0xffffffffu, r1, own_lane);
-        if (j + 1 < sg.j1) ok = load_quad(own, own, 0, 2, 4, 6, false);
-        // Q.K^T(j) is done: the rope slot is free, and after the last block Q.
-        if (ok) ok = warp_wait_all(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma);
-        if (ok && j + 1 < sg.j1) load_rope(own);
-        const bool tail = static_cast<int64_t>(j + 1) * kTreeBlock > sg.len;
-        if (ok && tail && lane == 0) mbar_arrive_expect_tx(bar(kTreeTail), 4 * S::STAGE);
-        if (ok) ok = load_quad(ra, rb, 2 * rank, 2 * rank, 4 + 2 * rank, 4 + 2 * rank, tail);
+        const int e3 = entry_of(j + 3);
+        const int other = __shfl_sync(0xffffffffu, r0, other_lane);
+        const int own1 = __shfl_sync(0xffffffffu, r1, own_lane), own2 = __shfl_sync(0xffffffffu, r2, own_lane);
+        // Q.K^T(j) is done: its groups, the rope chunk and after the last block Q.
+        if (!(ok = warp_wait_all(bar(kTreeSFull), g & 1, ab, kErrWaitMma))) break;
+        load_values(other, static_cast<int64_t>(j + 1) * kTreeBlock > sg.len);
+        if (j + 1 < sg.j1) load_rope(own1);
+        if (j + 2 < sg.j1) ok = load_keys(own2);
         r0 = r1;
+        r1 = r2;
+        r2 = row_of(j + 3, e3);
       }
     }
     if (!ok) spin_ns(2000000);  // let issued loads land before the CTA can exit
@@ -413,44 +432,51 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       const uint64_t drope = smem_desc_sw128(smem_u32(smem + S::ROPE), 16, 1024);
       const uint64_t dq = smem_desc_sw128(smem_u32(smem + S::Q), 16, 1024);
       const uint64_t dp = smem_desc_sw128(smem_u32(smem + S::P), 16, 1024);
-      const uint32_t full0 = bar(kTreeFull), empty0 = bar(kTreeEmpty), issue = elect_lane();
+      const uint32_t kfull0 = bar(kTreeKFull), vfull0 = bar(kTreeVFull), empty0 = bar(kTreeEmpty), issue = elect_lane();
       bool ok = true;
       int g = 0, seg = 0, commits = 0;
-      uint32_t quads = 0;  // runs of four stages so far
+      uint32_t ks = 0, kparity = 0, vs = 0, vparity = 0;  // the next groups of keys and of values
       auto qk = [&](int block) -> bool {
-        const uint32_t ts = tmem + kTreeColS + 64u * static_cast<uint32_t>(block & 1);
-        constexpr int kChunk = S::CHUNK >> 4, kStage = S::STAGE >> 4;
+        constexpr int kChunk = S::CHUNK >> 4, kGroup = S::GROUP >> 4;
+        const uint32_t ts = tmem + kTreeColS;
+        if (block > 0 && !mbar_wait(bar(kTreeSFree), (block - 1) & 1, ab, kErrWaitSoftmax)) return false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t s = (quads & 1) * 4 + i;
-          if (!mbar_wait(full0 + 8 * s, (quads >> 1) & 1, ab, kErrWaitTma)) return false;
+          if (i == 3) {  // the rope chunk before the group that lands last
+            if (!mbar_wait(bar(kTreeRopeFull), block & 1, ab, kErrWaitTma)) return false;
+            tc_fence_after();
+            umma_ss_pair_x4<2, 2>(ts, dq + (8 - S::Q_TMEM) * kChunk, drope, idesc_qk, 1u, issue);
+          }
+          if (!mbar_wait(kfull0 + 8 * ks, kparity, ab, kErrWaitTma)) return false;
           tc_fence_after();
-          const uint64_t k = dring + s * kStage;
-          umma_ss_pair_x4<2, 2>(ts, dq + i * kStage, k, idesc_qk, i > 0 ? 1u : 0u, issue);
-          umma_ss_pair_x4<2, 2>(ts, dq + i * kStage + kChunk, k + kChunk, idesc_qk, 1u, issue);
-          umma_commit_pair_warp(empty0 + 8 * s, 0x3, issue);
+          const uint64_t k = dring + ks * kGroup;
+          if (2 * i < S::Q_TMEM) {
+            umma_ts_pair_x4<2>(ts, tmem + kTreeColQ + 64 * i, k, idesc_qk, i > 0 ? 1u : 0u, issue);
+            umma_ts_pair_x4<2>(ts, tmem + kTreeColQ + 64 * i + 32, k + kChunk, idesc_qk, 1u, issue);
+          } else {
+            const uint64_t a = dq + (2 * i - S::Q_TMEM) * kChunk;
+            umma_ss_pair_x4<2, 2>(ts, a, k, idesc_qk, 1u, issue);
+            umma_ss_pair_x4<2, 2>(ts, a + kChunk, k + kChunk, idesc_qk, 1u, issue);
+          }
+          if (++ks == S::GROUPS) ks = 0, kparity ^= 1;
         }
-        ++quads;
-        if (!mbar_wait(bar(kTreeRopeFull), block & 1, ab, kErrWaitTma)) return false;
-        tc_fence_after();
-        umma_ss_pair_x4<2, 2>(ts, dq + 8 * kChunk, drope, idesc_qk, 1u, issue);
-        umma_commit_pair_warp(bar(kTreeSFull + (block & 1)), 0x3, issue);
+        umma_commit_pair_warp(bar(kTreeSFull), 0x3, issue);
         ++commits;
         return true;
       };
       auto pv = [&](int block, bool fresh) -> bool {
-        if (!mbar_wait_cluster(bar(kTreePFull), block & 1, ab, kErrWaitSoftmax)) return false;
-        constexpr int kChunk = S::CHUNK >> 4, kStage = S::STAGE >> 4;
+        constexpr int kChunk = S::CHUNK >> 4, kGroup = S::GROUP >> 4;
+        if (!mbar_wait(bar(kTreePFull), block & 1, ab, kErrWaitSoftmax)) return false;
+        tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // values [256 (i / 2), + 256) of keys [64 (i % 2), + 64)
-          const uint32_t s = (quads & 1) * 4 + i;
-          if (!mbar_wait(full0 + 8 * s, (quads >> 1) & 1, ab, kErrWaitTma)) return false;
+          if (!mbar_wait(vfull0 + 8 * vs, vparity, ab, kErrWaitTma)) return false;
           tc_fence_after();
-          umma_ss_pair_x4<2, 128>(tmem + 128u * (i >> 1), dp + (i & 1) * kChunk, dring_mn + s * kStage, idesc_pv,
+          umma_ss_pair_x4<2, 128>(tmem + 128u * (i >> 1), dp + (i & 1) * kChunk, dring_mn + vs * kGroup, idesc_pv,
                                   (!fresh || (i & 1)) ? 1u : 0u, issue);
-          umma_commit_pair_warp(empty0 + 8 * s, 0x3, issue);
+          umma_commit_pair_warp(empty0 + 8 * vs, 0x3, issue);
+          if (++vs == S::GROUPS) vs = 0, vparity ^= 1;
         }
-        ++quads;
         umma_commit_pair_warp(bar(kTreePVDone), 0x3, issue);
         ++commits;
         return true;
@@ -458,6 +484,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       while (ok && work.next(p, sg)) {
         const int n = sg.j1 - sg.j0;
         if (!(ok = mbar_wait(bar(kTreeQFull), seg & 1, ab, kErrWaitTma))) break;
+        if (!(ok = mbar_wait(bar(kTreeQReady), seg & 1, ab, kErrWaitSoftmax))) break;
         tc_fence_after();
         ok = qk(g);
         for (int j = 0; ok && j < n; ++j) {
@@ -470,18 +497,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       if (!ok && commits > 0) {
         umma_commit_pair_warp(bar(kTreeDrain), 0x1, issue);
         mbar_wait_drain(bar(kTreeDrain), 0);
-      }
-    } else if (lane == 0) {
-      // ---------------- the other CTA: its P (and the zeroed slots) handed on
-      // to the leader's issuer with one cluster-scope release per block, which
-      // would cost each softmax warp about a microsecond
-      bool ok = true;
-      int g = 0;
-      while (ok && work.next(p, sg)) {
-        for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
-          if (!(ok = mbar_wait(bar(kTreePLocal), g & 1, ab, kErrWaitSoftmax))) break;
-          mbar_arrive_cluster(mapa_shared(bar(kTreePFull), 0));
-        }
       }
     }
   } else {
@@ -496,8 +511,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
     float* xchg = reinterpret_cast<float*>(smem + S::XCHG);
     uint8_t* prow = smem + S::P + lh * S::CHUNK + row * 128;
     const float c = p.scale_log2;
+    const uint32_t p_full = mapa_shared(bar(kTreePFull), 0), s_free = mapa_shared(bar(kTreeSFree), 0);
     bool ok = true;
-    int g = 0, tails = 0, turn = 0, st = 0;
+    int g = 0, tails = 0, turn = 0;
     // The four threads' values of this row.
     auto exchange = [&](float v, float (&all)[4]) {
       float* x = xchg + (turn & 1) * 256;
@@ -507,7 +523,29 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
 #pragma unroll
       for (int i = 0; i < 4; ++i) all[i] = x[i * 64 + row];
     };
-    while (work.next(p, sg)) {
+    // The first six chunks of Q into tensor memory: with M = 128 both lane r and
+    // lane r + 64 hold row r; this warp's three chunks of its lanes' rows.
+    auto load_q = [&](const TreeSeg& of) {
+      const int64_t qr = static_cast<int64_t>(of.b) * p.N * p.H + of.tile * kTreeRows + 64 * rank + row;
+      const bool there = qr < static_cast<int64_t>(p.B) * p.N * p.H;
+      const uint4* src = reinterpret_cast<const uint4*>(p.qabs + (there ? qr : 0) * 512 + 192 * ch);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        uint32_t v[32];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint4 w = there ? __ldg(src + 8 * i + k) : make_uint4(0u, 0u, 0u, 0u);
+          v[4 * k] = w.x, v[4 * k + 1] = w.y, v[4 * k + 2] = w.z, v[4 * k + 3] = w.w;
+        }
+        tmem_st32(tl + kTreeColQ + 96u * ch + 32u * i, v);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(mapa_shared(bar(kTreeQReady), 0));
+    };
+    bool more = work.next(p, sg);
+    if (more) load_q(sg);
+    while (more) {
       const int r = sg.tile * kTreeRows + 64 * rank + row;  // row of the sequence: node * H + head
       const int live = sg.nodes * p.H;
       const bool has_tail = static_cast<int64_t>(sg.j1) * kTreeBlock > sg.len;
@@ -515,10 +553,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       const int total = sg.len + sg.nodes;
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = sg.j0; j < sg.j1; ++j, ++g) {
-        if (ok) ok = warp_wait_all(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma);
+        if (ok) ok = warp_wait_all(bar(kTreeSFull), g & 1, ab, kErrWaitMma);
         tc_fence_after();
         float x[32];
-        tmem_ld32(tl + kTreeColS + 64u * (g & 1) + 32u * ch, *reinterpret_cast<uint32_t(*)[32]>(x));
+        tmem_ld32(tl + kTreeColS + 32u * ch, *reinterpret_cast<uint32_t(*)[32]>(x));
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive_remote(s_free);
         const int64_t t0 = static_cast<int64_t>(j) * kTreeBlock;
         const bool tail = t0 + kTreeBlock > sg.len;
         if (tail) {
@@ -588,10 +629,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
           if (ok) {
             const int who = static_cast<int>(threadIdx.x) - 64;  // 256 threads: piece who % 32 of key who / 32
             const int piece = who & 31, h = piece >> 4, chunk = (piece >> 3) & 1;
-            // The run's stages: four for its first block's keys, then per block the next one's keys and its values.
-            const int sv = st + 8 * (j - sg.j0) + (j + 1 < sg.j1 ? 8 : 4);
             for (int k = static_cast<int>(max(int64_t(0), sg.len - t0)) + (who >> 5); k < kTreeBlock; k += 8) {
-              uint4* at = reinterpret_cast<uint4*>(smem + S::RING + ((sv + 2 * h + (k >> 6)) & (S::STAGES - 1)) * S::STAGE +
+              uint4* at = reinterpret_cast<uint4*>(smem + S::RING + (4 * g + 2 * h + (k >> 6)) % S::GROUPS * S::GROUP +
                                                    chunk * S::CHUNK + (k & 63) * 128 + (piece & 7) * 16);
               uint4 v = *at;
               uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -611,20 +650,29 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar(rank == 0 ? kTreePFull : kTreePLocal));
+        // P (and the zeroed values) is in this SM's own shared memory, where its
+        // tensor core reads it: each lane's fence has put its stores before that
+        // before lane 0 arrives. A cluster-scope release here, which orders them
+        // for the other SM's threads too, took 1300 to 2100 clk a block.
+        if (ok && lane == 0) mbar_arrive_remote(p_full);
       }
-      st += 8 * (sg.j1 - sg.j0);
-      // ---------------- the run's result: o_lat, or its part of it
+      // ---------------- the run's result: o_lat, or its part of it. The next
+      // run's Q first: its products have no more use for this one's.
+      TreeSeg nx = {};
+      more = work.next(p, nx);
+      if (more && ok) load_q(nx);
       float all[4];
       exchange(l_run, all);
       if (ok) ok = warp_wait_all(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma);
+      const TreeSeg sg_done = sg;
+      sg = nx;
       if (!ok) continue;
       tc_fence_after();
       const float l = (all[0] + all[1]) + (all[2] + all[3]);
       const int v0 = 256 * ch + 128 * lh;  // this thread's 128 of the 512 values
-      if (sg.j1 - sg.j0 == sg.blocks) {
+      if (sg_done.j1 - sg_done.j0 == sg_done.blocks) {
         const float inv = l != 0.f ? 1.f / l : 0.f;
-        uint4* dst = reinterpret_cast<uint4*>(p.olat + ((static_cast<int64_t>(sg.b) * p.N) * p.H + r) * 512 + v0);
+        uint4* dst = reinterpret_cast<uint4*>(p.olat + ((static_cast<int64_t>(sg_done.b) * p.N) * p.H + r) * 512 + v0);
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += 32) {
           uint32_t o[32];
@@ -640,7 +688,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
           }
         }
       } else {
-        const int slot = 2 * pair + (sg.first ? 0 : 1);
+        const int slot = 2 * pair + (sg_done.first ? 0 : 1);
         const int tr = 64 * rank + row;
         float* dst = p.part_o + static_cast<int64_t>(slot) * kTreeSlotFloats + (v0 / 4 * kTreeRows + tr) * 4;
         if (part == 0) p.part_ml[slot * kTreeRows + tr] = make_float2(m_run, l);

@@ -1097,7 +1097,7 @@ int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pa
                           const void* q, const void* kv, const void* pe, const int32_t* table,
                           const int32_t* cache_len, const int32_t* n_nodes, const int32_t* parents, float scale,
                           cudaStream_t st) {
-  mla::TreeParams p;
+  mla::TreeParams p = {};
   p.B = d.B;
   p.N = d.T;
   p.H = d.H;
@@ -1110,6 +1110,7 @@ int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pa
   p.cache_len = cache_len;
   p.n_nodes = n_nodes;
   p.parents = parents;
+  p.qabs = reinterpret_cast<const __nv_bfloat16*>(ws_at(ws, lay.qabs));
   p.olat = reinterpret_cast<__nv_bfloat16*>(ws_at(ws, lay.olat));
   p.ustart = reinterpret_cast<int64_t*>(ws_at(ws, lay.tree_start));
   p.part_o = reinterpret_cast<float*>(ws_at(ws, lay.tree_o));
