@@ -129,12 +129,13 @@ __host__ __device__ __forceinline__ int64_t tree_share(int64_t units, int pair, 
 struct TreeSmem {
   static constexpr int CHUNK = 8192;               // [64 keys or rows x 64] bf16
   static constexpr int GROUP = 2 * CHUNK;
-  static constexpr int GROUPS = 11;
+  static constexpr int GROUPS = 10;
+  static constexpr int ROPES = 2;                  // blocks whose rope chunks fit
   static constexpr int Q_TMEM = 6;                 // chunks of Q in tensor memory, the first of the nine
   static constexpr int Q_CHUNKS = 9 - Q_TMEM;      // and in shared memory
   static constexpr int RING = 0;
   static constexpr int ROPE = RING + GROUPS * GROUP;
-  static constexpr int Q = ROPE + CHUNK;
+  static constexpr int Q = ROPE + ROPES * CHUNK;
   static constexpr int P = Q + Q_CHUNKS * CHUNK;   // two [64 rows x 64 keys] chunks
   static constexpr int XCHG = P + 2 * CHUNK;       // [2][4][64] floats
   static constexpr int BARS = XCHG + 2 * 4 * 64 * 4;
@@ -147,15 +148,18 @@ enum : int {
   kTreeKFull = 0,                               // (L) per group: the own keys' values landed in both CTAs
   kTreeVFull = kTreeKFull + TreeSmem::GROUPS,   // (L) per group: the other keys' values landed in the CTA that reloads it
   kTreeEmpty = kTreeVFull + TreeSmem::GROUPS,   // per group: the P.V that read it is done
-  kTreeSFull = kTreeEmpty + TreeSmem::GROUPS,   // Q.K^T of a block is done
-  kTreeSFree,                                   // (L) S is in the softmax warps' registers (sixteen warps)
+  // Q.K^T of a block is done; one barrier for even and one for odd blocks, since
+  // the next block's may be done before the producer looks for this one's.
+  kTreeSFull = kTreeEmpty + TreeSmem::GROUPS,
+  kTreeSFree = kTreeSFull + 2,                  // (L) S is in the softmax warps' registers (sixteen warps)
   kTreePVDone,                                  // P.V of a block is done
-  kTreeRopeFull,                                // (L) the rope chunk landed in both CTAs
-  kTreeQFull,                                   // (L) Q's shared-memory part landed in both CTAs
+  kTreeRopeFull,                                // (L) per rope slot: the chunk landed in both CTAs
+  kTreeQFull = kTreeRopeFull + TreeSmem::ROPES,                                   // (L) Q's shared-memory part landed in both CTAs
   kTreeQReady,                                  // (L) its tensor-memory part is written (sixteen warps)
   kTreePFull,                                   // (L) P of both CTAs is written (sixteen warps)
-  kTreeTail,                                    // the reloaded values of a block with drafted keys landed in this CTA
-  kTreeDrain,
+  kTreeTail,                                    // the reloaded values of a block with drafted keys landed in this
+                                                // CTA; two, taken in turn
+  kTreeDrain = kTreeTail + 2,
   kTreeBars
 };
 static_assert(8 * kTreeBars + 8 <= 384, "barriers, then the share's start at byte 384");
@@ -322,20 +326,27 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
     const uint32_t kfull0_leader = mapa_shared(kfull0, 0), vfull0_leader = mapa_shared(vfull0, 0);
     const int page_mask = (1 << p.page_shift) - 1;
     bool ok = true;
-    int g = 0;                    // blocks so far
+    int g = 0, tails = 0;         // blocks so far, and those with drafted keys
     uint32_t ks = 0, parity = 0;  // the next group of keys
     uint32_t vs = 0;              // the next group of values
-    // Table entry of box `lane` (of a block's 128 keys) of block j; -1 behind the last position.
+    // Box `lane` of a block's 128 keys: whether block j has it, its table entry
+    // (fetched two blocks ahead and not looked at before row_of, so that the
+    // warp does not wait for it), and its cache row; a box behind the last
+    // position reads zeros from behind the cache.
+    auto has_box = [&](int j) -> bool {
+      const int64_t t = static_cast<int64_t>(j) * kTreeBlock + (static_cast<int64_t>(lane) << p.box_shift);
+      return lane < (2 << box_log) && j < sg.j1 && t < sg.len + sg.nodes;
+    };
     auto entry_of = [&](int j) -> int {
       const int64_t t = static_cast<int64_t>(j) * kTreeBlock + (static_cast<int64_t>(lane) << p.box_shift);
-      if (lane >= (2 << box_log) || j >= sg.j1 || t >= sg.len + sg.nodes) return -1;
-      const int e = __ldg(p.table + static_cast<int64_t>(sg.b) * p.table_width + (t >> p.page_shift));
-      return e < 0 ? INT32_MIN : e;  // -1 is ours
+      int e = 0;
+      if (has_box(j)) e = __ldg(p.table + static_cast<int64_t>(sg.b) * p.table_width + (t >> p.page_shift));
+      return e;
     };
-    // Its cache row; nothing to read: a row behind the cache, which loads zeros.
     auto row_of = [&](int j, int entry) -> int {
+      if (!has_box(j)) return cache_rows;
       if (entry < 0 || entry >= p.num_pages) {
-        if (entry != -1) atomicCAS(p.err, 0, kErrPage);
+        atomicCAS(p.err, 0, kErrPage);
         return cache_rows;
       }
       return (entry << p.page_shift) + ((j * kTreeBlock + (lane << p.box_shift)) & page_mask);
@@ -353,10 +364,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       return true;
     };
     // The other keys' values, rows `other`, over the groups this CTA is done
-    // with. With `tail` the bytes count on this CTA's kTreeTail, and "P is
+    // with. With `tail` the bytes count on a barrier of this CTA, and "P is
     // written" tells the issuer that they have landed.
     auto load_values = [&](int other, bool tail) {
-      if (tail && lane == 0) mbar_arrive_expect_tx(bar(kTreeTail), 2 * S::GROUP);
+      const uint32_t landed = bar(kTreeTail + (tails & 1));
+      if (tail && lane == 0) mbar_arrive_expect_tx(landed, 2 * S::GROUP);
+      tails += tail ? 1 : 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (rank == 0 && lane == 0) {
@@ -369,19 +382,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         if (loads && (i & 1) != rank) {
           const int col = (4 * (i >> 1) + 2 * rank + chunk) * 64;
           if (tail)
-            tma_load_2d(dst0 + vs * S::GROUP, &tm_kv, bar(kTreeTail), col, other);
+            tma_load_2d(dst0 + vs * S::GROUP, &tm_kv, landed, col, other);
           else
             tma_load_2d_pair(dst0 + vs * S::GROUP, &tm_kv, vfull0_leader + 8 * vs, col, other);
         }
         if (++vs == S::GROUPS) vs = 0;
       }
     };
-    auto load_rope = [&](int own) {
-      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(kTreeRopeFull), 2 * S::CHUNK);
+    const uint32_t rope0 = smem_u32(smem + S::ROPE) + (bx << (p.box_shift + 7));
+    const uint32_t rfull0 = bar(kTreeRopeFull), rfull0_leader = mapa_shared(rfull0, 0);
+    auto load_rope = [&](int block, int own) {
+      const uint32_t x = static_cast<uint32_t>(block) % S::ROPES;
+      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(rfull0 + 8 * x, 2 * S::CHUNK);
       __syncwarp();
-      if (chunk == 0)
-        tma_load_2d_pair(smem_u32(smem + S::ROPE) + (bx << (p.box_shift + 7)), &tm_pe,
-                         mapa_shared(bar(kTreeRopeFull), 0), 0, own);
+      if (chunk == 0) tma_load_2d_pair(rope0 + x * S::CHUNK, &tm_pe, rfull0_leader + 8 * x, 0, own);
     };
     const int own_lane = (rank << box_log) + bx, other_lane = ((rank ^ 1) << box_log) + bx;
     while (ok && work.next(p, sg)) {
@@ -401,19 +415,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       // r<k>: cache rows (per lane) of block j + k; e3: table entries of block j + 3.
       const int e1 = entry_of(sg.j0 + 1), e2 = entry_of(sg.j0 + 2);
       int r0 = row_of(sg.j0, entry_of(sg.j0)), r1 = row_of(sg.j0 + 1, e1), r2 = row_of(sg.j0 + 2, e2);
-      int own = __shfl_sync(0xffffffffu, r0, own_lane);
-      ok = load_keys(own);
-      if (ok) load_rope(own);
-      if (ok && sg.j0 + 1 < sg.j1) ok = load_keys(__shfl_sync(0xffffffffu, r1, own_lane));
+      const int first = __shfl_sync(0xffffffffu, r0, own_lane), second = __shfl_sync(0xffffffffu, r1, own_lane);
+      load_rope(g, first);
+      ok = load_keys(first);
+      if (ok && sg.j0 + 1 < sg.j1) {
+        load_rope(g + 1, second);
+        ok = load_keys(second);
+      }
       for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
         const int e3 = entry_of(j + 3);
         const int other = __shfl_sync(0xffffffffu, r0, other_lane);
-        const int own1 = __shfl_sync(0xffffffffu, r1, own_lane), own2 = __shfl_sync(0xffffffffu, r2, own_lane);
-        // Q.K^T(j) is done: its groups, the rope chunk and after the last block Q.
-        if (!(ok = warp_wait_all(bar(kTreeSFull), g & 1, ab, kErrWaitMma))) break;
+        const int own2 = __shfl_sync(0xffffffffu, r2, own_lane);
+        // Q.K^T(j) is done: with its groups, its rope slot and after the last block Q.
+        if (!(ok = warp_wait_all(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma))) break;
         load_values(other, static_cast<int64_t>(j + 1) * kTreeBlock > sg.len);
-        if (j + 1 < sg.j1) load_rope(own1);
-        if (j + 2 < sg.j1) ok = load_keys(own2);
+        if (j + 2 < sg.j1) {
+          load_rope(g + 2, own2);
+          ok = load_keys(own2);
+        }
         r0 = r1;
         r1 = r2;
         r2 = row_of(j + 3, e3);
@@ -443,9 +462,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (i == 3) {  // the rope chunk before the group that lands last
-            if (!mbar_wait(bar(kTreeRopeFull), block & 1, ab, kErrWaitTma)) return false;
+            const uint32_t x = static_cast<uint32_t>(block) % S::ROPES;
+            if (!mbar_wait(bar(kTreeRopeFull) + 8 * x, (block / S::ROPES) & 1, ab, kErrWaitTma)) return false;
             tc_fence_after();
-            umma_ss_pair_x4<2, 2>(ts, dq + (8 - S::Q_TMEM) * kChunk, drope, idesc_qk, 1u, issue);
+            umma_ss_pair_x4<2, 2>(ts, dq + (8 - S::Q_TMEM) * kChunk, drope + x * kChunk, idesc_qk, 1u, issue);
           }
           if (!mbar_wait(kfull0 + 8 * ks, kparity, ab, kErrWaitTma)) return false;
           tc_fence_after();
@@ -460,7 +480,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
           }
           if (++ks == S::GROUPS) ks = 0, kparity ^= 1;
         }
-        umma_commit_pair_warp(bar(kTreeSFull), 0x3, issue);
+        umma_commit_pair_warp(bar(kTreeSFull + (block & 1)), 0x3, issue);
         ++commits;
         return true;
       };
@@ -553,7 +573,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       const int total = sg.len + sg.nodes;
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = sg.j0; j < sg.j1; ++j, ++g) {
-        if (ok) ok = warp_wait_all(bar(kTreeSFull), g & 1, ab, kErrWaitMma);
+        if (ok) ok = warp_wait_all(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma);
         tc_fence_after();
         float x[32];
         tmem_ld32(tl + kTreeColS + 32u * ch, *reinterpret_cast<uint32_t(*)[32]>(x));
@@ -624,7 +644,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
           // position hold whatever the page held before, and 0 * NaN is
           // NaN, so they are zeroed; so is what is not finite in a drafted
           // key's values (a row that sees it gets its NaN from the score).
-          if (ok) ok = warp_wait_all(bar(kTreeTail), tails & 1, ab, kErrWaitTma);
+          if (ok) ok = warp_wait_all(bar(kTreeTail + (tails & 1)), (tails >> 1) & 1, ab, kErrWaitTma);
           ++tails;
           if (ok) {
             const int who = static_cast<int>(threadIdx.x) - 64;  // 256 threads: piece who % 32 of key who / 32

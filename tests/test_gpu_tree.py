@@ -293,6 +293,21 @@ def test_same_result_every_time_and_on_every_stream():
     _no_device_error()
 
 
+@pytest.mark.parametrize("N,H,page", [(1, 128, 64), (5, 64, 16), (64, 8, 128)])
+def test_many_runs_of_blocks_per_pair(N, H, page):
+    # every pair works through several sequences and tiles, with one and two blocks of drafted keys at their ends,
+    # many times over; tables too large to stay in the first-level cache
+    lens = [37 * (b % 50) + 1000 * (b % 7) + 64 * (b % 3) for b in range(150)]
+    p = Problem(lens, N, H, page=page)
+    first = p.run()
+    for _ in range(30):
+        again = p.run()
+    _no_device_error()
+    assert torch.equal(again, first)
+    some = [0, 1, 6, 49, 77, 149]
+    assert_near(first[some], p.expect(some)[some])
+
+
 def test_captured_graph_follows_its_inputs():
     p = Problem([500, 900], 4, 8)
     n0, nodes, table = p.i32(p.lens), p.i32(p.nodes), p.table.clone()
