@@ -20,30 +20,30 @@
 // Shape of the products. A pair UMMA with M = 128 gives each CTA 64 rows and
 // uses all 128 lanes of its tensor memory: lanes 0..63 hold columns [0, N/2) of
 // rows 0..63, lanes 64..127 columns [N/2, N). O (64 rows x 512 fp32) then takes
-// 256 of the 512 columns, where 128 rows in one CTA would take all of them
-// and leave none for S. Measured rates of the tensor core alone (clk per block
-// of 128 keys; full rate in brackets): P.V 1050 (1024); Q.K^T 1745 (1152), about
-// 47 clk per instruction whatever its N up to 128, the same with Q in tensor
-// memory; both one after the other 2490 (2176).
+// 256 of the 512 columns, where 128 rows in one CTA would take all of them and
+// leave none for S. Rates of the tensor core alone, clk per block of 128 keys
+// (full rate in brackets): Q.K^T 1161 (1152), P.V 1037 (1024), both 2190.
 //
-// A block costs 2.2k clk of tensor core but 136 KB per CTA if Q.K^T's keys and
-// P.V's values are loaded apart, and L2 -> SM then sets the pace (a block took
-// 4.1k clk; with half the bytes 2.9k). So a block is kept in place: for Q.K^T a
+// A block is 2.2k clk of tensor core, but 136 KB per CTA if Q.K^T's keys and
+// P.V's values are loaded apart, and L2 -> SM then sets the pace (4.1k clk a
+// block; 2.9k with half the bytes). So a block is kept in place: for Q.K^T a
 // CTA holds its own 64 of the block's keys, all 512 latent values of each, as
 // four 16 KB groups of 128 values; for P.V it needs all 128 keys, its own half
 // of each 256 values. The two meet: group i = 2 h + r of CTA r is already the
-// values [256 h + 128 r, + 128) of its own keys. The other two groups it is done
-// with once Q.K^T has read them, and loads them again with the other keys' values
-// of its half. Group 2 h + k then holds, in both CTAs, keys [64 k, + 64) of the
-// block, values of half h, and each CTA has loaded 13 chunks of 64 values instead
-// of 17. The price is that groups stay taken through the softmax: eleven fit,
-// which is 2.75 blocks, because six of Q's nine chunks live in tensor memory
-// (next to O and one S; Q.K^T(j + 1) waits until S(j) has been loaded, which P.V(j
-// - 1) covers).
+// values [256 h + 128 r, + 128) of its own keys. The other two groups it is
+// done with once Q.K^T has read them, and loads them again with the other keys'
+// values of its half. Group 2 h + k then holds, in both CTAs, keys [64 k, + 64)
+// of the block, values of half h, and each CTA has loaded 13 chunks of 64 values
+// instead of 17. The price is that groups stay taken through the softmax: ten
+// fit, two and a half blocks, because six of Q's nine chunks live in tensor
+// memory (next to O and one S; Q.K^T(j + 1) waits until S(j) has been loaded,
+// which P.V(j - 1) covers). Those six travel through the ring, too: three groups
+// in front of a run's first block, which the softmax warps copy.
 //
-// Roles (320 threads per CTA): warp 0 producer; warp 1 of the leader issues
-// the UMMAs; warps 2..9 softmax: four threads per row, one for each quarter of the block's keys, agree on the
-// running maximum through shared memory.
+// Roles (320 threads per CTA): warp 0 producer, requesting keys two blocks ahead
+// of values and across the ends of runs; warp 1 of the leader issues the UMMAs;
+// warps 2..9 softmax: four threads per row, one for each quarter of the block's
+// keys, agree on the running maximum through shared memory.
 #pragma once
 
 #include "gemm2.cuh"
@@ -67,7 +67,6 @@ struct TreeParams {
   const int32_t* cache_len;      // [B]
   const int32_t* n_nodes;        // [B], or nullptr: N each
   const int32_t* parents;        // [B][N], or nullptr: a chain
-  const __nv_bfloat16* qabs;     // [B*N][H][512]
   __nv_bfloat16* olat;           // [B*N][H][512]
   int64_t* ustart;               // [B + 1] first unit of each sequence, and their number
   float* part_o;                 // [2 pairs][128 value quads][128 rows][4] unnormalised partial tiles
@@ -101,7 +100,7 @@ struct TreeSeg {
 struct TreeWork {
   int64_t u0, u, u1, base;  // base: first unit of sequence b
   int b;
-  __device__ bool next(const TreeParams& p, TreeSeg& s) {
+  __device__ __noinline__ bool next(const TreeParams& p, TreeSeg& s) {
     if (u >= u1) return false;
     int tiles;
     while (true) {
@@ -132,6 +131,7 @@ struct TreeSmem {
   static constexpr int GROUPS = 10;
   static constexpr int ROPES = 2;                  // blocks whose rope chunks fit
   static constexpr int Q_TMEM = 6;                 // chunks of Q in tensor memory, the first of the nine
+  static constexpr int Q_GROUPS = Q_TMEM / 2;      // as groups of the ring
   static constexpr int Q_CHUNKS = 9 - Q_TMEM;      // and in shared memory
   static constexpr int RING = 0;
   static constexpr int ROPE = RING + GROUPS * GROUP;
@@ -155,7 +155,9 @@ enum : int {
   kTreePVDone,                                  // P.V of a block is done
   kTreeRopeFull,                                // (L) per rope slot: the chunk landed in both CTAs
   kTreeQFull = kTreeRopeFull + TreeSmem::ROPES,                                   // (L) Q's shared-memory part landed in both CTAs
-  kTreeQReady,                                  // (L) its tensor-memory part is written (sixteen warps)
+  kTreeQGroups,                                 // the three groups of its tensor-memory part landed in this CTA; two,
+                                                // taken in turn, since a run of one block is requested two runs ahead
+  kTreeQReady = kTreeQGroups + 2,                                // (L) they are in tensor memory (sixteen warps)
   kTreePFull,                                   // (L) P of both CTAs is written (sixteen warps)
   kTreeTail,                                    // the reloaded values of a block with drafted keys landed in this
                                                 // CTA; two, taken in turn
@@ -311,132 +313,169 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
   work.b = static_cast<int>(start[1]);
   const uint32_t tmem = *tmem_slot;
   const Abort ab{abort_word, p.err};
-  TreeSeg sg = {};
+  // The pair's next run, in registers (next() itself stays out of line).
+  auto next_run = [&](TreeSeg& run) -> bool {
+    TreeSeg t;
+    const bool more = work.next(p, t);
+    run = t;
+    return more;
+  };
 
   if (warp == 0) {
-    // ---------------- producer: the whole warp, each lane at most one box of a
-    // stage. It has about 250 clk per stage, so what a stage needs is computed
-    // once here, and table entries are fetched two blocks before their use.
-    const int box_log = 6 - p.box_shift;  // boxes per 64 keys, log2
-    const int bx = lane & ((1 << box_log) - 1), chunk = lane >> box_log;
-    const bool loads = chunk < 2;
+    // ---------------- producer: the whole warp on one path, one lane issues
+    // (tma_load_3d_pair_warp). It has about 200 clk per group of the ring.
+    // With pages of 64 keys or more a group is one box [2 chunks][64 keys][64];
+    // with smaller pages (box_log > 0) a chunk is 2^box_log boxes.
+    const int box_log = 6 - p.box_shift;
+    const int boxes = 1 << box_log;
+    const uint32_t box_bytes = 128u << p.box_shift;
     const int cache_rows = p.num_pages << p.page_shift;
-    const uint32_t dst0 = smem_u32(smem + S::RING) + chunk * S::CHUNK + (bx << (p.box_shift + 7));
+    const uint32_t ring0 = smem_u32(smem + S::RING), rope0 = smem_u32(smem + S::ROPE);
     const uint32_t kfull0 = bar(kTreeKFull), vfull0 = bar(kTreeVFull), empty0 = bar(kTreeEmpty);
     const uint32_t kfull0_leader = mapa_shared(kfull0, 0), vfull0_leader = mapa_shared(vfull0, 0);
+    const uint32_t rfull0 = bar(kTreeRopeFull), rfull0_leader = mapa_shared(rfull0, 0);
+    const uint32_t issue = elect_lane(), arm = rank == 0 ? issue : 0u;  // the leader arms the shared barriers
     const int page_mask = (1 << p.page_shift) - 1;
+    const int own0 = rank << box_log, other0 = (rank ^ 1) << box_log;  // lanes with the rows of the own and the other keys
     bool ok = true;
-    int g = 0, tails = 0;         // blocks so far, and those with drafted keys
-    uint32_t ks = 0, parity = 0;  // the next group of keys
-    uint32_t vs = 0;              // the next group of values
-    // Box `lane` of a block's 128 keys: whether block j has it, its table entry
-    // (fetched two blocks ahead and not looked at before row_of, so that the
-    // warp does not wait for it), and its cache row; a box behind the last
-    // position reads zeros from behind the cache.
-    auto has_box = [&](int j) -> bool {
-      const int64_t t = static_cast<int64_t>(j) * kTreeBlock + (static_cast<int64_t>(lane) << p.box_shift);
-      return lane < (2 << box_log) && j < sg.j1 && t < sg.len + sg.nodes;
+    uint32_t ks = 0, parity = 0;  // the next group to fill
+    uint32_t vs = 0;              // the next group to fill again with values
+    int ahead = 0, runs = 0, tails = 0;  // blocks and runs requested; blocks with drafted keys whose values are
+    // Keys run two blocks ahead of values, across the ends of runs: block kj of
+    // run sg is the next one.
+    TreeSeg sg = {};
+    bool more = next_run(sg);
+    int kj = sg.j0;
+    // Box `lane` of a block's 128 keys: whether the next block of keys has it,
+    // its table entry (fetched a block ahead, and not looked at before row_of,
+    // so that the warp does not wait for it), and its cache row; a box behind
+    // the last position reads zeros from behind the cache.
+    auto has_box = [&]() -> bool {
+      const int64_t t = static_cast<int64_t>(kj) * kTreeBlock + (static_cast<int64_t>(lane) << p.box_shift);
+      return more && lane < 2 * boxes && t < sg.len + sg.nodes;
     };
-    auto entry_of = [&](int j) -> int {
-      const int64_t t = static_cast<int64_t>(j) * kTreeBlock + (static_cast<int64_t>(lane) << p.box_shift);
+    auto entry_of = [&]() -> int {
+      const int64_t t = static_cast<int64_t>(kj) * kTreeBlock + (static_cast<int64_t>(lane) << p.box_shift);
       int e = 0;
-      if (has_box(j)) e = __ldg(p.table + static_cast<int64_t>(sg.b) * p.table_width + (t >> p.page_shift));
+      if (has_box()) e = __ldg(p.table + static_cast<int64_t>(sg.b) * p.table_width + (t >> p.page_shift));
       return e;
     };
-    auto row_of = [&](int j, int entry) -> int {
-      if (!has_box(j)) return cache_rows;
+    auto row_of = [&](int entry) -> int {
+      if (!has_box()) return cache_rows;
       if (entry < 0 || entry >= p.num_pages) {
         atomicCAS(p.err, 0, kErrPage);
         return cache_rows;
       }
-      return (entry << p.page_shift) + ((j * kTreeBlock + (lane << p.box_shift)) & page_mask);
+      return (entry << p.page_shift) + ((kj * kTreeBlock + (lane << p.box_shift)) & page_mask);
     };
-    // A block's own keys, rows `own` (per lane).
-    auto load_keys = [&](int own) -> bool {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (!warp_wait_all(empty0 + 8 * ks, parity ^ 1, ab, kErrWaitConsumer)) return false;
-        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(kfull0 + 8 * ks, 2 * S::GROUP);
-        __syncwarp();
-        if (loads) tma_load_2d_pair(dst0 + ks * S::GROUP, &tm_kv, kfull0_leader + 8 * ks, (2 * i + chunk) * 64, own);
-        if (++ks == S::GROUPS) ks = 0, parity ^= 1;
-      }
-      return true;
-    };
-    // The other keys' values, rows `other`, over the groups this CTA is done
-    // with. With `tail` the bytes count on a barrier of this CTA, and "P is
-    // written" tells the issuer that they have landed.
-    auto load_values = [&](int other, bool tail) {
-      const uint32_t landed = bar(kTreeTail + (tails & 1));
-      if (tail && lane == 0) mbar_arrive_expect_tx(landed, 2 * S::GROUP);
-      tails += tail ? 1 : 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (rank == 0 && lane == 0) {
-          if (tail)
-            mbar_arrive(vfull0 + 8 * vs);
-          else
-            mbar_arrive_expect_tx(vfull0 + 8 * vs, S::GROUP);
+    // Chunks 2 * pair_of and the next of 64 keys, whose rows are in lanes from
+    // lane0 on, into group s.
+    auto load_group = [&](uint32_t s, int pair_of, int rows, int lane0, uint32_t barrier) {
+      const uint32_t dst = ring0 + s * S::GROUP;
+      if (box_log == 0) {
+        tma_load_3d_pair_warp(dst, &tm_kv, barrier, 0, __shfl_sync(0xffffffffu, rows, lane0), 2 * pair_of, issue);
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < boxes; ++x) {
+          const int row = __shfl_sync(0xffffffffu, rows, lane0 + x);
+          tma_load_3d_pair_warp(dst + x * box_bytes, &tm_kv, barrier, 0, row, 2 * pair_of, issue);
+          tma_load_3d_pair_warp(dst + S::CHUNK + x * box_bytes, &tm_kv, barrier, 0, row, 2 * pair_of + 1, issue);
         }
-        __syncwarp();
-        if (loads && (i & 1) != rank) {
-          const int col = (4 * (i >> 1) + 2 * rank + chunk) * 64;
-          if (tail)
-            tma_load_2d(dst0 + vs * S::GROUP, &tm_kv, landed, col, other);
-          else
-            tma_load_2d_pair(dst0 + vs * S::GROUP, &tm_kv, vfull0_leader + 8 * vs, col, other);
-        }
-        if (++vs == S::GROUPS) vs = 0;
       }
     };
-    const uint32_t rope0 = smem_u32(smem + S::ROPE) + (bx << (p.box_shift + 7));
-    const uint32_t rfull0 = bar(kTreeRopeFull), rfull0_leader = mapa_shared(rfull0, 0);
-    auto load_rope = [&](int block, int own) {
-      const uint32_t x = static_cast<uint32_t>(block) % S::ROPES;
-      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(rfull0 + 8 * x, 2 * S::CHUNK);
-      __syncwarp();
-      if (chunk == 0) tma_load_2d_pair(rope0 + x * S::CHUNK, &tm_pe, rfull0_leader + 8 * x, 0, own);
+    // A requested block: its rows, whether it has drafted keys, whether its keys
+    // are still to be asked for, and the first query row of its run if it is the
+    // run's first block.
+    struct Block {
+      int row, qrow;
+      bool there, tail, late;
     };
-    const int own_lane = (rank << box_log) + bx, other_lane = ((rank ^ 1) << box_log) + bx;
-    while (ok && work.next(p, sg)) {
-      // Q: rows of this tile; those past the sequence's last belong to another
-      // sequence or to none, and are not stored. The previous run's products
-      // are done: its last block's S was waited for below.
-      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(bar(kTreeQFull), 2 * S::Q_CHUNKS * S::CHUNK);
-      __syncwarp();
-      if (lane < S::Q_CHUNKS) {
-        const int qrow = (sg.b * p.N) * p.H + sg.tile * kTreeRows + 64 * rank;
-        const uint32_t d = smem_u32(smem + S::Q) + lane * S::CHUNK, qb = mapa_shared(bar(kTreeQFull), 0);
-        if (lane + S::Q_TMEM < 8)
-          tma_load_2d_pair(d, &tm_qabs, qb, (lane + S::Q_TMEM) * 64, qrow);
-        else
-          tma_load_2d_pair(d, &tm_q, qb, 128, qrow);
-      }
-      // r<k>: cache rows (per lane) of block j + k; e3: table entries of block j + 3.
-      const int e1 = entry_of(sg.j0 + 1), e2 = entry_of(sg.j0 + 2);
-      int r0 = row_of(sg.j0, entry_of(sg.j0)), r1 = row_of(sg.j0 + 1, e1), r2 = row_of(sg.j0 + 2, e2);
-      const int first = __shfl_sync(0xffffffffu, r0, own_lane), second = __shfl_sync(0xffffffffu, r1, own_lane);
-      load_rope(g, first);
-      ok = load_keys(first);
-      if (ok && sg.j0 + 1 < sg.j1) {
-        load_rope(g + 1, second);
-        ok = load_keys(second);
-      }
-      for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
-        const int e3 = entry_of(j + 3);
-        const int other = __shfl_sync(0xffffffffu, r0, other_lane);
-        const int own2 = __shfl_sync(0xffffffffu, r2, own_lane);
-        // Q.K^T(j) is done: with its groups, its rope slot and after the last block Q.
+    Block b0 = {}, b1 = {}, b2 = {};
+    int entry = entry_of();
+#pragma unroll 1
+    for (int g = -2; g < 0 || b0.there; ++g) {
+      if (b0.there) {
+        // Q.K^T of block g is done: with its groups, its rope slot and, if the
+        // next block begins a run, Q.
         if (!(ok = warp_wait_all(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma))) break;
-        load_values(other, static_cast<int64_t>(j + 1) * kTreeBlock > sg.len);
-        if (j + 2 < sg.j1) {
-          load_rope(g + 2, own2);
-          ok = load_keys(own2);
+        // The other keys' values, over the groups this CTA is done with. With
+        // `tail` the bytes count on a barrier of this CTA, and "P is written"
+        // tells the issuer that they have landed.
+        const uint32_t landed = mapa_shared(bar(kTreeTail + (tails & 1)), rank);
+        if (b0.tail) {
+          mbar_arrive_expect_tx_warp(bar(kTreeTail + (tails & 1)), 2 * S::GROUP, issue);
+          ++tails;
         }
-        r0 = r1;
-        r1 = r2;
-        r2 = row_of(j + 3, e3);
+        if (b0.qrow >= 0) vs = (vs + S::Q_GROUPS) % S::GROUPS;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          mbar_arrive_expect_tx_warp(vfull0 + 8 * vs, b0.tail ? 0 : S::GROUP, arm);
+          if ((i & 1) != rank)
+            load_group(vs, 2 * (i >> 1) + rank, b0.row, other0, b0.tail ? landed : vfull0_leader + 8 * vs);
+          if (++vs == S::GROUPS) vs = 0;
+        }
       }
+      if (b1.late) {
+        // The next block begins a run: Q's shared-memory part. Rows past the
+        // sequence's last belong to another sequence or to none, and are not stored.
+        const uint32_t d = smem_u32(smem + S::Q), qb = mapa_shared(bar(kTreeQFull), 0);
+        mbar_arrive_expect_tx_warp(bar(kTreeQFull), 2 * S::Q_CHUNKS * S::CHUNK, arm);
+        tma_load_3d_pair_warp(d, &tm_qabs, qb, 0, b1.qrow, S::Q_TMEM, issue);
+        tma_load_2d_pair_warp(d + 2 * S::CHUNK, &tm_q, qb, 128, b1.qrow, issue);
+      }
+      // Keys: of block g + 1 if it begins a run, then of block g + 2 unless it
+      // does. Then only its Q's groups are requested now: with its keys as well,
+      // this warp would come to wait for the P.V of a block whose values it has
+      // not yet asked for.
+#pragma unroll 1
+      for (int k = b1.late ? 0 : 1; ok && k < 2; ++k) {
+        if (k == 1) {
+          b2.there = more;
+          b2.late = more && kj == sg.j0;
+          if (!more) break;
+          b2.row = row_of(entry);
+          b2.tail = static_cast<int64_t>(kj + 1) * kTreeBlock > sg.len;
+          b2.qrow = b2.late ? sg.b * p.N * p.H + sg.tile * kTreeRows + 64 * rank : -1;
+          if (b2.late) {
+            const uint32_t landed = bar(kTreeQGroups + (runs++ & 1));
+            mbar_arrive_expect_tx_warp(landed, S::Q_GROUPS * S::GROUP, issue);
+#pragma unroll 1
+            for (int i = 0; i < S::Q_GROUPS; ++i) {
+              if (!(ok = warp_wait_all(empty0 + 8 * ks, parity ^ 1, ab, kErrWaitConsumer))) break;
+              // the ring's barriers keep step: nobody waits for these two
+              mbar_arrive_expect_tx_warp(kfull0 + 8 * ks, 0, arm);
+              mbar_arrive_expect_tx_warp(vfull0 + 8 * ks, 0, arm);
+              tma_load_3d_pair_warp(ring0 + ks * S::GROUP, &tm_qabs, mapa_shared(landed, rank), 0, b2.qrow, 2 * i, issue);
+              if (++ks == S::GROUPS) ks = 0, parity ^= 1;
+            }
+            break;
+          }
+        }
+        const int rows = k == 0 ? b1.row : b2.row;
+        const uint32_t x = static_cast<uint32_t>(ahead++) % S::ROPES;  // free: the block two before is through Q.K^T
+        mbar_arrive_expect_tx_warp(rfull0 + 8 * x, 2 * S::CHUNK, arm);
+#pragma unroll 1
+        for (int i = 0; i < boxes; ++i)
+          tma_load_2d_pair_warp(rope0 + x * S::CHUNK + i * box_bytes, &tm_pe, rfull0_leader + 8 * x, 0,
+                                __shfl_sync(0xffffffffu, rows, own0 + i), issue);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          if (!(ok = warp_wait_all(empty0 + 8 * ks, parity ^ 1, ab, kErrWaitConsumer))) break;
+          mbar_arrive_expect_tx_warp(kfull0 + 8 * ks, 2 * S::GROUP, arm);
+          load_group(ks, i, rows, own0, kfull0_leader + 8 * ks);
+          if (++ks == S::GROUPS) ks = 0, parity ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (b2.there) {
+        if (++kj == sg.j1) {
+          more = next_run(sg);
+          kj = sg.j0;
+        }
+        entry = entry_of();
+      }
+      b0 = b1;
+      b1 = b2;
     }
     if (!ok) spin_ns(2000000);  // let issued loads land before the CTA can exit
   } else if (warp == 1) {
@@ -458,16 +497,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       auto qk = [&](int block) -> bool {
         constexpr int kChunk = S::CHUNK >> 4, kGroup = S::GROUP >> 4;
         const uint32_t ts = tmem + kTreeColS;
-        if (block > 0 && !mbar_wait(bar(kTreeSFree), (block - 1) & 1, ab, kErrWaitSoftmax)) return false;
+        if (block > 0 && !mbar_wait_short(bar(kTreeSFree), (block - 1) & 1, ab, kErrWaitSoftmax)) return false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (i == 3) {  // the rope chunk before the group that lands last
             const uint32_t x = static_cast<uint32_t>(block) % S::ROPES;
-            if (!mbar_wait(bar(kTreeRopeFull) + 8 * x, (block / S::ROPES) & 1, ab, kErrWaitTma)) return false;
+            if (!mbar_wait_short(bar(kTreeRopeFull) + 8 * x, (block / S::ROPES) & 1, ab, kErrWaitTma)) return false;
             tc_fence_after();
             umma_ss_pair_x4<2, 2>(ts, dq + (8 - S::Q_TMEM) * kChunk, drope + x * kChunk, idesc_qk, 1u, issue);
           }
-          if (!mbar_wait(kfull0 + 8 * ks, kparity, ab, kErrWaitTma)) return false;
+          if (!mbar_wait_short(kfull0 + 8 * ks, kparity, ab, kErrWaitTma)) return false;
           tc_fence_after();
           const uint64_t k = dring + ks * kGroup;
           if (2 * i < S::Q_TMEM) {
@@ -486,11 +525,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       };
       auto pv = [&](int block, bool fresh) -> bool {
         constexpr int kChunk = S::CHUNK >> 4, kGroup = S::GROUP >> 4;
-        if (!mbar_wait(bar(kTreePFull), block & 1, ab, kErrWaitSoftmax)) return false;
+        if (!mbar_wait_short(bar(kTreePFull), block & 1, ab, kErrWaitSoftmax)) return false;
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // values [256 (i / 2), + 256) of keys [64 (i % 2), + 64)
-          if (!mbar_wait(vfull0 + 8 * vs, vparity, ab, kErrWaitTma)) return false;
+          if (!mbar_wait_short(vfull0 + 8 * vs, vparity, ab, kErrWaitTma)) return false;
           tc_fence_after();
           umma_ss_pair_x4<2, 128>(tmem + 128u * (i >> 1), dp + (i & 1) * kChunk, dring_mn + vs * kGroup, idesc_pv,
                                   (!fresh || (i & 1)) ? 1u : 0u, issue);
@@ -501,15 +540,21 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         ++commits;
         return true;
       };
-      while (ok && work.next(p, sg)) {
+      TreeSeg sg = {};
+      while (ok && next_run(sg)) {
         const int n = sg.j1 - sg.j0;
-        if (!(ok = mbar_wait(bar(kTreeQFull), seg & 1, ab, kErrWaitTma))) break;
-        if (!(ok = mbar_wait(bar(kTreeQReady), seg & 1, ab, kErrWaitSoftmax))) break;
+        if (!(ok = mbar_wait_short(bar(kTreeQFull), seg & 1, ab, kErrWaitTma))) break;
+        if (!(ok = mbar_wait_short(bar(kTreeQReady), seg & 1, ab, kErrWaitSoftmax))) break;
+        for (int i = 0; i < S::Q_GROUPS; ++i) {  // Q's groups are free: nothing else has read them
+          umma_commit_pair_warp(empty0 + 8 * ks, 0x3, issue);
+          if (++ks == S::GROUPS) ks = 0, kparity ^= 1;
+          if (++vs == S::GROUPS) vs = 0, vparity ^= 1;
+        }
         tc_fence_after();
-        ok = qk(g);
-        for (int j = 0; ok && j < n; ++j) {
+#pragma unroll 1
+        for (int j = -1; ok && j < n; ++j) {
           if (j + 1 < n) ok = qk(g + j + 1);
-          if (ok) ok = pv(g + j, j == 0);
+          if (ok && j >= 0) ok = pv(g + j, j == 0);
         }
         g += n;
         ++seg;
@@ -533,7 +578,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
     const float c = p.scale_log2;
     const uint32_t p_full = mapa_shared(bar(kTreePFull), 0), s_free = mapa_shared(bar(kTreeSFree), 0);
     bool ok = true;
-    int g = 0, tails = 0, turn = 0;
+    int g = 0, tails = 0, turn = 0, runs = 0;  // runs: whose Q has been loaded
     // The four threads' values of this row.
     auto exchange = [&](float v, float (&all)[4]) {
       float* x = xchg + (turn & 1) * 256;
@@ -543,28 +588,33 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
 #pragma unroll
       for (int i = 0; i < 4; ++i) all[i] = x[i * 64 + row];
     };
-    // The first six chunks of Q into tensor memory: with M = 128 both lane r and
-    // lane r + 64 hold row r; this warp's three chunks of its lanes' rows.
-    auto load_q = [&](const TreeSeg& of) {
-      const int64_t qr = static_cast<int64_t>(of.b) * p.N * p.H + of.tile * kTreeRows + 64 * rank + row;
-      const bool there = qr < static_cast<int64_t>(p.B) * p.N * p.H;
-      const uint4* src = reinterpret_cast<const uint4*>(p.qabs + (there ? qr : 0) * 512 + 192 * ch);
+    // Q's groups (positions `at` and on of the ring) into tensor memory: with M =
+    // 128 both lane r and lane r + 64 hold row r; this warp's three chunks of
+    // its lanes' rows.
+    auto load_q = [&](int at) -> bool {
+      if (!warp_wait_all(bar(kTreeQGroups + (runs & 1)), (runs >> 1) & 1, ab, kErrWaitTma)) return false;
+      ++runs;
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
+        const int c = 3 * ch + i;
+        const uint8_t* src = smem + S::RING + (at + (c >> 1)) % S::GROUPS * S::GROUP + (c & 1) * S::CHUNK + row * 128;
         uint32_t v[32];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint4 w = there ? __ldg(src + 8 * i + k) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 w = *reinterpret_cast<const uint4*>(src + ((k ^ (row & 7)) << 4));
           v[4 * k] = w.x, v[4 * k + 1] = w.y, v[4 * k + 2] = w.z, v[4 * k + 3] = w.w;
         }
-        tmem_st32(tl + kTreeColQ + 96u * ch + 32u * i, v);
+        tmem_st32(tl + kTreeColQ + 32u * c, v);
       }
+      fence_proxy_async_smem();  // the groups are filled again by TMA
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(mapa_shared(bar(kTreeQReady), 0));
+      return true;
     };
-    bool more = work.next(p, sg);
-    if (more) load_q(sg);
+    TreeSeg sg = {};
+    bool more = next_run(sg);
+    if (more) ok = load_q(0);
     while (more) {
       const int r = sg.tile * kTreeRows + 64 * rank + row;  // row of the sequence: node * H + head
       const int live = sg.nodes * p.H;
@@ -650,7 +700,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
             const int who = static_cast<int>(threadIdx.x) - 64;  // 256 threads: piece who % 32 of key who / 32
             const int piece = who & 31, h = piece >> 4, chunk = (piece >> 3) & 1;
             for (int k = static_cast<int>(max(int64_t(0), sg.len - t0)) + (who >> 5); k < kTreeBlock; k += 8) {
-              uint4* at = reinterpret_cast<uint4*>(smem + S::RING + (4 * g + 2 * h + (k >> 6)) % S::GROUPS * S::GROUP +
+              uint4* at = reinterpret_cast<uint4*>(smem + S::RING + (S::Q_GROUPS * runs + 4 * g + 2 * h + (k >> 6)) % S::GROUPS * S::GROUP +
                                                    chunk * S::CHUNK + (k & 63) * 128 + (piece & 7) * 16);
               uint4 v = *at;
               uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -679,8 +729,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       // ---------------- the run's result: o_lat, or its part of it. The next
       // run's Q first: its products have no more use for this one's.
       TreeSeg nx = {};
-      more = work.next(p, nx);
-      if (more && ok) load_q(nx);
+      more = next_run(nx);
+      if (more && ok) ok = load_q(4 * g + S::Q_GROUPS * runs);
       float all[4];
       exchange(l_run, all);
       if (ok) ok = warp_wait_all(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma);
@@ -738,55 +788,72 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
 // Joins the tiles that several pairs shared, and zeroes the rows of nodes that
 // are not there. Thread: one row of a tile, 16 of its values; with M the
 // largest of the parts' maxima, o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p
-// over the pairs p whose shares meet the tile, in their order.
+// over the pairs p whose shares meet the tile, in their order. The pairs are
+// found side by side, one per thread: each takes two 64-bit divisions, which in
+// a row took 40 us for a tile of eight parts.
 constexpr int kTreeJoinThreads = 256;
 constexpr int kTreeJoinBlocks = kTreeRows * 32 / kTreeJoinThreads;  // per tile
+static_assert(kTreeMaxPairs <= 96, "three warps look for the parts");
 
 __global__ void __launch_bounds__(kTreeJoinThreads)
 tree_combine_kernel(const TreeParams p, int pairs) {
+  __shared__ int slots[96];
+  __shared__ int found[3];
   const int all_tiles = (p.N * p.H + kTreeRows - 1) / kTreeRows;
   const int at = static_cast<int>(blockIdx.x) / kTreeJoinBlocks, b = at / all_tiles, tile = at % all_tiles;
   const int item = static_cast<int>(blockIdx.x) % kTreeJoinBlocks * kTreeJoinThreads + static_cast<int>(threadIdx.x);
   const int tr = item & 127, v0 = (item >> 7) * 16;
   const int r = tile * kTreeRows + tr;
-  if (r >= p.N * p.H) return;
   int len, nodes, tiles, blocks;
   tree_lengths(p, b, len, nodes);
   tree_extent(p, len, nodes, tiles, blocks);
-  uint4* dst = reinterpret_cast<uint4*>(p.olat + ((static_cast<int64_t>(b) * p.N) * p.H + r) * 512 + v0);
+  // Part of pair c, if it has one, in the order of the pairs.
+  const int c = static_cast<int>(threadIdx.x);
+  int slot = -1;
+  if (c < 96) {
+    if (c < pairs && tile < tiles) {
+      const int64_t units = p.ustart[p.B], lo = p.ustart[b] + static_cast<int64_t>(tile) * blocks, hi = lo + blocks;
+      const int64_t s0 = tree_share(units, c, pairs), s1 = tree_share(units, c + 1, pairs);
+      if (s1 > s0 && s1 > lo && s0 < hi && !(s0 <= lo && s1 >= hi)) slot = 2 * c + (s0 >= lo ? 0 : 1);
+    }
+    const uint32_t mine = __ballot_sync(0xffffffffu, slot >= 0);
+    if ((c & 31) == 0) found[c >> 5] = static_cast<int>(mine);
+  }
+  __syncthreads();
+  const int n0 = __popc(found[0]), n1 = __popc(found[1]), n = n0 + n1 + __popc(found[2]);
+  if (slot >= 0)
+    slots[(c >= 64 ? n0 + n1 : c >= 32 ? n0 : 0) + __popc(static_cast<uint32_t>(found[c >> 5]) & ((1u << (c & 31)) - 1))] = slot;
+  __syncthreads();
+  if (r >= p.N * p.H) return;
+  uint4* dst = reinterpret_cast<uint4*>(p.olat + (static_cast<int64_t>(b) * p.N * p.H + r) * 512 + v0);
   if (r >= nodes * p.H) {
     dst[0] = dst[1] = make_uint4(0u, 0u, 0u, 0u);
     return;
   }
-  const int64_t units = p.ustart[p.B], lo = p.ustart[b] + static_cast<int64_t>(tile) * blocks, hi = lo + blocks;
-  int c0 = static_cast<int>(lo * pairs / units);
-  while (tree_share(units, c0 + 1, pairs) <= lo) ++c0;
-  if (tree_share(units, c0 + 1, pairs) >= hi) return;  // one pair's alone
+  if (n == 0) return;  // one pair's alone
   float M = -INFINITY;
-  for (int c = c0; c < pairs && tree_share(units, c, pairs) < hi; ++c) {
-    const int64_t s = tree_share(units, c, pairs);
-    if (tree_share(units, c + 1, pairs) > s) M = fmaxf(M, p.part_ml[(2 * c + (s >= lo ? 0 : 1)) * kTreeRows + tr].x);
-  }
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) M = fmaxf(M, p.part_ml[slots[i] * kTreeRows + tr].x);
   float acc[16], sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int c = c0; c < pairs && tree_share(units, c, pairs) < hi; ++c) {
-    const int64_t s = tree_share(units, c, pairs);
-    if (tree_share(units, c + 1, pairs) <= s) continue;
-    const int slot = 2 * c + (s >= lo ? 0 : 1);
-    const float2 ml = p.part_ml[slot * kTreeRows + tr];
+#pragma unroll 2
+  for (int i = 0; i < n; ++i) {
+    const float2 ml = p.part_ml[slots[i] * kTreeRows + tr];
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(slots[i]) * kTreeSlotFloats) +
+                        v0 / 4 * kTreeRows + tr;
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = src[k * kTreeRows];
     if (ml.y == 0.f) continue;  // saw none of its keys
     const float w = ex2_approx(ml.x - M);
     sum = fmaf(w, ml.y, sum);
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(slot) * kTreeSlotFloats) +
-                        v0 / 4 * kTreeRows + tr;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = src[i * kTreeRows];
-      acc[4 * i] = fmaf(w, v.x, acc[4 * i]);
-      acc[4 * i + 1] = fmaf(w, v.y, acc[4 * i + 1]);
-      acc[4 * i + 2] = fmaf(w, v.z, acc[4 * i + 2]);
-      acc[4 * i + 3] = fmaf(w, v.w, acc[4 * i + 3]);
+    for (int k = 0; k < 4; ++k) {
+      acc[4 * k] = fmaf(w, v[k].x, acc[4 * k]);
+      acc[4 * k + 1] = fmaf(w, v[k].y, acc[4 * k + 1]);
+      acc[4 * k + 2] = fmaf(w, v[k].z, acc[4 * k + 2]);
+      acc[4 * k + 3] = fmaf(w, v[k].w, acc[4 * k + 3]);
     }
   }
   const float inv = sum != 0.f ? 1.f / sum : 0.f;

@@ -217,6 +217,19 @@ bool map_3d_bt(CUtensorMap* m, const void* base, uint64_t inner, uint64_t T, uin
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 matrix [rows, 512] as 64-column chunks, [rows][8][64]: a box is
+// box_chunks chunks of box_rows rows, each chunk contiguous in shared memory;
+// rows past the last read as zero.
+bool map_chunks(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows, uint32_t box_chunks) {
+  const cuuint64_t dims[3] = {64, rows, 8};
+  const cuuint64_t strides[2] = {1024, 128};
+  const cuuint32_t box[3] = {64, box_rows, box_chunks};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // How e4m3 weights meet bf16 activations (mla_set_e4m3_weight_conversion):
 // 0 = dequantised into a bf16 workspace copy per call, 1 = converted on chip
 // by the projection GEMMs.
@@ -1110,7 +1123,6 @@ int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pa
   p.cache_len = cache_len;
   p.n_nodes = n_nodes;
   p.parents = parents;
-  p.qabs = reinterpret_cast<const __nv_bfloat16*>(ws_at(ws, lay.qabs));
   p.olat = reinterpret_cast<__nv_bfloat16*>(ws_at(ws, lay.olat));
   p.ustart = reinterpret_cast<int64_t*>(ws_at(ws, lay.tree_start));
   p.part_o = reinterpret_cast<float*>(ws_at(ws, lay.tree_o));
@@ -1119,9 +1131,9 @@ int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pa
   const uint64_t qrows = static_cast<uint64_t>(d.B) * d.T * d.H, crows = static_cast<uint64_t>(pg.num_pages) * pg.page_size;
   const uint32_t box = 1u << p.box_shift;
   CUtensorMap tkv, tpe, tqa, tq;
-  if (!map_2d(&tkv, kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kL, crows, kL * 2, 64, box) ||
+  if (!map_chunks(&tkv, kv, crows, box, box == 64 ? 2 : 1) ||
       !map_2d(&tpe, pe, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDr, crows, kDr * 2, 64, box) ||
-      !map_2d(&tqa, ws_at(ws, lay.qabs), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kL, qrows, kL * 2, 64, 64) ||
+      !map_chunks(&tqa, ws_at(ws, lay.qabs), qrows, 64, 2) ||
       !map_2d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDn + kDr, qrows, (kDn + kDr) * 2, 64, 64))
     return MLA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};

@@ -170,10 +170,21 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const A
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// mbar_wait with everything but the first try out of line: a kernel whose warps
+// run different roles with a dozen waits each outgrows the instruction caches
+// when every wait brings its timeout along.
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* flag, int* err, int code) {
+  return mbar_wait(bar, parity, Abort{flag, err}, code);
+}
+
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, const Abort& ab, int code) {
+  return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity, ab.flag, ab.err, code);
+}
+
 // Every lane waits; true if all saw the phase complete (64 clk when it already
 // has, against 155 with one lane waiting and a shuffle).
 __device__ __forceinline__ bool warp_wait_all(uint32_t bar, uint32_t parity, const Abort& ab, int code) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, code)) != 0;
+  return __all_sync(0xffffffffu, mbar_wait_short(bar, parity, ab, code)) != 0;
 }
 
 // Bounded wait used while draining after an abort: never records an error.
@@ -530,6 +541,36 @@ __device__ __forceinline__ void umma_ts_pair_x4(uint32_t d_tmem, uint32_t a_tmem
       "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, t;\n\t"
       "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate_first), "r"(issue), "n"(DB), "n"(2 * DB), "n"(3 * DB)
+      : "memory");
+}
+
+// TMA loads and an mbarrier arrival for a converged warp, issued by the lane with
+// `issue` set: with lane-dependent operands the compiler would issue them lane
+// by lane in a loop.
+__device__ __forceinline__ void tma_load_2d_pair_warp(uint32_t dst, const CUtensorMap* m, uint32_t bar_cluster, int c0,
+                                                      int c1, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(m), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(issue)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair_warp(uint32_t dst, const CUtensorMap* m, uint32_t bar_cluster, int c0,
+                                                      int c1, int c2, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(m), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "r"(issue)
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_expect_tx_warp(uint32_t bar, uint32_t bytes, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(issue)
       : "memory");
 }
 
