@@ -40,9 +40,8 @@
 // which P.V(j - 1) covers). Those six travel through the ring, too: three groups
 // in front of a run's first block, which the softmax warps copy.
 //
-// Roles (320 threads per CTA): warp 0 producer, requesting keys two blocks ahead
-// of values and across the ends of runs; warp 1 of the leader issues the UMMAs;
-// warps 2..9 softmax: four threads per row, one for each quarter of the block's
+// Roles (352 threads per CTA): warps 0 and 10 producers, of keys and of values;
+// warp 1 of the leader issues the UMMAs; warps 2..9 softmax: four threads per row, one for each quarter of the block's
 // keys, agree on the running maximum through shared memory.
 #pragma once
 
@@ -55,7 +54,7 @@ constexpr int kTreeMax = 64;        // nodes per sequence: one bit each
 constexpr int kTreeRows = 128;      // rows of a tile
 constexpr int kTreeBlock = 128;     // keys of a block
 constexpr int kTreeMaxPairs = 74;   // pairs a launch uses at most (148 SMs); the workspace is sized for them
-constexpr int kTreeThreads = 320;
+constexpr int kTreeThreads = 352;
 constexpr int kTreeSlotFloats = kTreeRows * 512;  // one partial tile
 
 struct TreeParams {
@@ -321,161 +320,133 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
     return more;
   };
 
-  if (warp == 0) {
-    // ---------------- producer: the whole warp on one path, one lane issues
-    // (tma_load_3d_pair_warp). It has about 200 clk per group of the ring.
-    // With pages of 64 keys or more a group is one box [2 chunks][64 keys][64];
-    // with smaller pages (box_log > 0) a chunk is 2^box_log boxes.
-    const int box_log = 6 - p.box_shift;
-    const int boxes = 1 << box_log;
+  if (warp == 0 || warp == kTreeThreads / 32 - 1) {
+    // ---------------- producers: whole warps on one path, one lane issues
+    // (tma_load_3d_pair_warp). Warp 0 asks for keys (and Q's groups in front of a
+    // run's), as far ahead as the ring has room; the last warp for the other
+    // keys' values once Q.K^T is done (and for the rest of Q). With pages of 64
+    // keys or more a group is one box [2 chunks][64 keys][64]; with smaller ones a
+    // chunk is 64 / page boxes.
+    const int half = warp == 0 ? rank : rank ^ 1;  // which 64 keys of a block this warp loads
+    const int box_log = 6 - p.box_shift, boxes = 1 << box_log;
     const uint32_t box_bytes = 128u << p.box_shift;
-    const int cache_rows = p.num_pages << p.page_shift;
-    const uint32_t ring0 = smem_u32(smem + S::RING), rope0 = smem_u32(smem + S::ROPE);
-    const uint32_t kfull0 = bar(kTreeKFull), vfull0 = bar(kTreeVFull), empty0 = bar(kTreeEmpty);
-    const uint32_t kfull0_leader = mapa_shared(kfull0, 0), vfull0_leader = mapa_shared(vfull0, 0);
-    const uint32_t rfull0 = bar(kTreeRopeFull), rfull0_leader = mapa_shared(rfull0, 0);
+    const int cache_rows = p.num_pages << p.page_shift, page_mask = (1 << p.page_shift) - 1;
+    const uint32_t ring0 = smem_u32(smem + S::RING);
+    const uint32_t kfull0 = bar(kTreeKFull), vfull0 = bar(kTreeVFull);
     const uint32_t issue = elect_lane(), arm = rank == 0 ? issue : 0u;  // the leader arms the shared barriers
-    const int page_mask = (1 << p.page_shift) - 1;
-    const int own0 = rank << box_log, other0 = (rank ^ 1) << box_log;  // lanes with the rows of the own and the other keys
-    bool ok = true;
-    uint32_t ks = 0, parity = 0;  // the next group to fill
-    uint32_t vs = 0;              // the next group to fill again with values
-    int ahead = 0, runs = 0, tails = 0;  // blocks and runs requested; blocks with drafted keys whose values are
-    // Keys run two blocks ahead of values, across the ends of runs: block kj of
-    // run sg is the next one.
-    TreeSeg sg = {};
-    bool more = next_run(sg);
-    int kj = sg.j0;
-    // Box `lane` of a block's 128 keys: whether the next block of keys has it,
-    // its table entry (fetched a block ahead, and not looked at before row_of,
-    // so that the warp does not wait for it), and its cache row; a box behind
-    // the last position reads zeros from behind the cache.
-    auto has_box = [&]() -> bool {
-      const int64_t t = static_cast<int64_t>(kj) * kTreeBlock + (static_cast<int64_t>(lane) << p.box_shift);
-      return more && lane < 2 * boxes && t < sg.len + sg.nodes;
+    // Box `lane` of this warp's 64 keys of block j: whether the run has it, its
+    // table entry (fetched a block ahead, and not looked at before row_of, so
+    // that the warp does not wait for it), and its cache row; a box behind the
+    // last position reads zeros from behind the cache.
+    auto place = [&](int j) -> int64_t {
+      return static_cast<int64_t>(j) * kTreeBlock + 64 * half + (static_cast<int64_t>(lane) << p.box_shift);
     };
-    auto entry_of = [&]() -> int {
-      const int64_t t = static_cast<int64_t>(kj) * kTreeBlock + (static_cast<int64_t>(lane) << p.box_shift);
+    TreeSeg sg = {};
+    auto entry_of = [&](int j) -> int {
       int e = 0;
-      if (has_box()) e = __ldg(p.table + static_cast<int64_t>(sg.b) * p.table_width + (t >> p.page_shift));
+      if (lane < boxes && j < sg.j1 && place(j) < sg.len + sg.nodes)
+        e = __ldg(p.table + static_cast<int64_t>(sg.b) * p.table_width + (place(j) >> p.page_shift));
       return e;
     };
-    auto row_of = [&](int entry) -> int {
-      if (!has_box()) return cache_rows;
+    auto row_of = [&](int j, int entry) -> int {
+      if (lane >= boxes || place(j) >= sg.len + sg.nodes) return cache_rows;
       if (entry < 0 || entry >= p.num_pages) {
         atomicCAS(p.err, 0, kErrPage);
         return cache_rows;
       }
-      return (entry << p.page_shift) + ((kj * kTreeBlock + (lane << p.box_shift)) & page_mask);
+      return (entry << p.page_shift) + static_cast<int>(place(j) & page_mask);
     };
-    // Chunks 2 * pair_of and the next of 64 keys, whose rows are in lanes from
-    // lane0 on, into group s.
-    auto load_group = [&](uint32_t s, int pair_of, int rows, int lane0, uint32_t barrier) {
+    // Chunks 2 * pair_of and the next of the 64 keys whose rows the lanes hold, into group s.
+    auto load_group = [&](uint32_t s, int pair_of, int rows, uint32_t barrier) {
       const uint32_t dst = ring0 + s * S::GROUP;
       if (box_log == 0) {
-        tma_load_3d_pair_warp(dst, &tm_kv, barrier, 0, __shfl_sync(0xffffffffu, rows, lane0), 2 * pair_of, issue);
+        tma_load_3d_pair_warp(dst, &tm_kv, barrier, 0, __shfl_sync(0xffffffffu, rows, 0), 2 * pair_of, issue);
       } else {
 #pragma unroll 1
         for (int x = 0; x < boxes; ++x) {
-          const int row = __shfl_sync(0xffffffffu, rows, lane0 + x);
+          const int row = __shfl_sync(0xffffffffu, rows, x);
           tma_load_3d_pair_warp(dst + x * box_bytes, &tm_kv, barrier, 0, row, 2 * pair_of, issue);
           tma_load_3d_pair_warp(dst + S::CHUNK + x * box_bytes, &tm_kv, barrier, 0, row, 2 * pair_of + 1, issue);
         }
       }
     };
-    // A requested block: its rows, whether it has drafted keys, whether its keys
-    // are still to be asked for, and the first query row of its run if it is the
-    // run's first block.
-    struct Block {
-      int row, qrow;
-      bool there, tail, late;
-    };
-    Block b0 = {}, b1 = {}, b2 = {};
-    int entry = entry_of();
+    bool ok = true;
+    int g = 0, runs = 0;  // blocks and runs so far
+    if (warp == 0) {
+      const uint32_t rope0 = smem_u32(smem + S::ROPE), empty0 = bar(kTreeEmpty), rfull0 = bar(kTreeRopeFull);
+      const uint32_t kfull0_leader = mapa_shared(kfull0, 0), rfull0_leader = mapa_shared(rfull0, 0);
+      uint32_t ks = 0, parity = 0;  // the next group to fill
+      while (ok && next_run(sg)) {
+        int entry = entry_of(sg.j0);
+        const int qrow = sg.b * p.N * p.H + sg.tile * kTreeRows + 64 * rank;
+        const uint32_t landed = bar(kTreeQGroups + (runs++ & 1));
+        mbar_arrive_expect_tx_warp(landed, S::Q_GROUPS * S::GROUP, issue);
 #pragma unroll 1
-    for (int g = -2; g < 0 || b0.there; ++g) {
-      if (b0.there) {
-        // Q.K^T of block g is done: with its groups, its rope slot and, if the
-        // next block begins a run, Q.
-        if (!(ok = warp_wait_all(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma))) break;
-        // The other keys' values, over the groups this CTA is done with. With
-        // `tail` the bytes count on a barrier of this CTA, and "P is written"
-        // tells the issuer that they have landed.
-        const uint32_t landed = mapa_shared(bar(kTreeTail + (tails & 1)), rank);
-        if (b0.tail) {
-          mbar_arrive_expect_tx_warp(bar(kTreeTail + (tails & 1)), 2 * S::GROUP, issue);
-          ++tails;
-        }
-        if (b0.qrow >= 0) vs = (vs + S::Q_GROUPS) % S::GROUPS;
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          mbar_arrive_expect_tx_warp(vfull0 + 8 * vs, b0.tail ? 0 : S::GROUP, arm);
-          if ((i & 1) != rank)
-            load_group(vs, 2 * (i >> 1) + rank, b0.row, other0, b0.tail ? landed : vfull0_leader + 8 * vs);
-          if (++vs == S::GROUPS) vs = 0;
-        }
-      }
-      if (b1.late) {
-        // The next block begins a run: Q's shared-memory part. Rows past the
-        // sequence's last belong to another sequence or to none, and are not stored.
-        const uint32_t d = smem_u32(smem + S::Q), qb = mapa_shared(bar(kTreeQFull), 0);
-        mbar_arrive_expect_tx_warp(bar(kTreeQFull), 2 * S::Q_CHUNKS * S::CHUNK, arm);
-        tma_load_3d_pair_warp(d, &tm_qabs, qb, 0, b1.qrow, S::Q_TMEM, issue);
-        tma_load_2d_pair_warp(d + 2 * S::CHUNK, &tm_q, qb, 128, b1.qrow, issue);
-      }
-      // Keys: of block g + 1 if it begins a run, then of block g + 2 unless it
-      // does. Then only its Q's groups are requested now: with its keys as well,
-      // this warp would come to wait for the P.V of a block whose values it has
-      // not yet asked for.
-#pragma unroll 1
-      for (int k = b1.late ? 0 : 1; ok && k < 2; ++k) {
-        if (k == 1) {
-          b2.there = more;
-          b2.late = more && kj == sg.j0;
-          if (!more) break;
-          b2.row = row_of(entry);
-          b2.tail = static_cast<int64_t>(kj + 1) * kTreeBlock > sg.len;
-          b2.qrow = b2.late ? sg.b * p.N * p.H + sg.tile * kTreeRows + 64 * rank : -1;
-          if (b2.late) {
-            const uint32_t landed = bar(kTreeQGroups + (runs++ & 1));
-            mbar_arrive_expect_tx_warp(landed, S::Q_GROUPS * S::GROUP, issue);
-#pragma unroll 1
-            for (int i = 0; i < S::Q_GROUPS; ++i) {
-              if (!(ok = warp_wait_all(empty0 + 8 * ks, parity ^ 1, ab, kErrWaitConsumer))) break;
-              // the ring's barriers keep step: nobody waits for these two
-              mbar_arrive_expect_tx_warp(kfull0 + 8 * ks, 0, arm);
-              mbar_arrive_expect_tx_warp(vfull0 + 8 * ks, 0, arm);
-              tma_load_3d_pair_warp(ring0 + ks * S::GROUP, &tm_qabs, mapa_shared(landed, rank), 0, b2.qrow, 2 * i, issue);
-              if (++ks == S::GROUPS) ks = 0, parity ^= 1;
-            }
-            break;
-          }
-        }
-        const int rows = k == 0 ? b1.row : b2.row;
-        const uint32_t x = static_cast<uint32_t>(ahead++) % S::ROPES;  // free: the block two before is through Q.K^T
-        mbar_arrive_expect_tx_warp(rfull0 + 8 * x, 2 * S::CHUNK, arm);
-#pragma unroll 1
-        for (int i = 0; i < boxes; ++i)
-          tma_load_2d_pair_warp(rope0 + x * S::CHUNK + i * box_bytes, &tm_pe, rfull0_leader + 8 * x, 0,
-                                __shfl_sync(0xffffffffu, rows, own0 + i), issue);
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; ok && i < S::Q_GROUPS; ++i) {
           if (!(ok = warp_wait_all(empty0 + 8 * ks, parity ^ 1, ab, kErrWaitConsumer))) break;
-          mbar_arrive_expect_tx_warp(kfull0 + 8 * ks, 2 * S::GROUP, arm);
-          load_group(ks, i, rows, own0, kfull0_leader + 8 * ks);
+          mbar_arrive_expect_tx_warp(kfull0 + 8 * ks, 0, arm);  // keep step with the ring: nobody waits for these two
+          mbar_arrive_expect_tx_warp(vfull0 + 8 * ks, 0, arm);
+          tma_load_3d_pair_warp(ring0 + ks * S::GROUP, &tm_qabs, mapa_shared(landed, rank), 0, qrow, 2 * i, issue);
           if (++ks == S::GROUPS) ks = 0, parity ^= 1;
         }
-      }
-      if (!ok) break;
-      if (b2.there) {
-        if (++kj == sg.j1) {
-          more = next_run(sg);
-          kj = sg.j0;
+#pragma unroll 1
+        for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
+          const int rows = row_of(j, entry);
+          entry = entry_of(j + 1);
+          // The rope slot: Q.K^T of the block two before has read it.
+          if (g >= 2 && !(ok = warp_wait_all(bar(kTreeSFull + (g & 1)), ((g - 2) >> 1) & 1, ab, kErrWaitMma))) break;
+          const uint32_t x = static_cast<uint32_t>(g) % S::ROPES;
+          mbar_arrive_expect_tx_warp(rfull0 + 8 * x, 2 * S::CHUNK, arm);
+#pragma unroll 1
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d_pair_warp(rope0 + x * S::CHUNK + i * box_bytes, &tm_pe, rfull0_leader + 8 * x, 0,
+                                  __shfl_sync(0xffffffffu, rows, i), issue);
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            if (!(ok = warp_wait_all(empty0 + 8 * ks, parity ^ 1, ab, kErrWaitConsumer))) break;
+            mbar_arrive_expect_tx_warp(kfull0 + 8 * ks, 2 * S::GROUP, arm);
+            load_group(ks, i, rows, kfull0_leader + 8 * ks);
+            if (++ks == S::GROUPS) ks = 0, parity ^= 1;
+          }
         }
-        entry = entry_of();
       }
-      b0 = b1;
-      b1 = b2;
+    } else {
+      const uint32_t vfull0_leader = mapa_shared(vfull0, 0), qfull_leader = mapa_shared(bar(kTreeQFull), 0);
+      const uint32_t q0 = smem_u32(smem + S::Q);
+      uint32_t vs = 0;  // the next group to fill again
+      int tails = 0;    // blocks with drafted keys so far
+      while (ok && next_run(sg)) {
+        int entry = entry_of(sg.j0);
+        // Q's shared-memory part: Q.K^T of the run before is done. Rows past the
+        // sequence's last belong to another sequence or to none, and are not stored.
+        const int qrow = sg.b * p.N * p.H + sg.tile * kTreeRows + 64 * rank;
+        mbar_arrive_expect_tx_warp(bar(kTreeQFull), 2 * S::Q_CHUNKS * S::CHUNK, arm);
+        tma_load_3d_pair_warp(q0, &tm_qabs, qfull_leader, 0, qrow, S::Q_TMEM, issue);
+        tma_load_2d_pair_warp(q0 + 2 * S::CHUNK, &tm_q, qfull_leader, 128, qrow, issue);
+        vs = (vs + S::Q_GROUPS) % S::GROUPS;
+#pragma unroll 1
+        for (int j = sg.j0; j < sg.j1; ++j, ++g) {
+          const int rows = row_of(j, entry);
+          entry = entry_of(j + 1);
+          if (!(ok = warp_wait_all(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma))) break;
+          // Over the groups this CTA is done with. In a block with drafted keys
+          // the bytes count on a barrier of this CTA, and "P is written" tells the
+          // issuer that they have landed.
+          const bool tail = static_cast<int64_t>(j + 1) * kTreeBlock > sg.len;
+          const uint32_t landed = bar(kTreeTail + (tails & 1));
+          if (tail) {
+            mbar_arrive_expect_tx_warp(landed, 2 * S::GROUP, issue);
+            ++tails;
+          }
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            mbar_arrive_expect_tx_warp(vfull0 + 8 * vs, tail ? 0 : S::GROUP, arm);
+            if ((i & 1) != rank)
+              load_group(vs, 2 * (i >> 1) + rank, rows, tail ? mapa_shared(landed, rank) : vfull0_leader + 8 * vs);
+            if (++vs == S::GROUPS) vs = 0;
+          }
+        }
+      }
     }
     if (!ok) spin_ns(2000000);  // let issued loads land before the CTA can exit
   } else if (warp == 1) {
