@@ -295,11 +295,15 @@ def mla_quantize_act(x, codes=None, scales=None, stream=None):
 # ------------------------------------------------------------------ serving over a paged cache
 
 
+# These calls take a few microseconds on the device at the smallest sizes, so their host side is kept short.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream's handle without its object
+
+
 def _expect(t, name, dtype, shape=None):
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _call(name, device, stream, args, used=()):
@@ -313,20 +317,24 @@ def _call(name, device, stream, args, used=()):
             raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
         for t in used:
             t.record_stream(stream)
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(device.index)
     else:
-        stream = torch.cuda.current_stream(device)
+        handle = torch.cuda.current_stream(device).cuda_stream
     if device.index == torch.cuda.current_device():
-        rc = fn(*args, stream.cuda_stream)
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream)
-    _check(name, rc)
+            rc = fn(*args, handle)
+    if rc != 0:
+        raise MlaError(name, rc)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
+def _same_device(device, *tensors):
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+            raise ValueError(f"the tensors are on {device} and {t.device}")
 
 
 def make_rope(base=10000.0, layout=MLA_ROPE_INTERLEAVED, scaling=MLA_ROPE_UNSCALED, factor=1.0, original_len=4096,
@@ -343,20 +351,27 @@ def make_rope(base=10000.0, layout=MLA_ROPE_INTERLEAVED, scaling=MLA_ROPE_UNSCAL
 def _rows_and_heads(t, lead):
     """(rows, row stride, heads, head stride) of a tensor [*lead, H, W] or [*lead, W] whose last dimension is
     contiguous and whose leading ones fold into one."""
-    if t.dim() not in (lead + 1, lead + 2) or t.stride(-1) != 1:
-        raise ValueError("the tensor must be [*positions.shape, heads, width] or [*positions.shape, width], its last "
-                         "dimension contiguous")
-    heads, head_stride = (t.shape[-2], t.stride(-2)) if t.dim() == lead + 2 else (1, t.shape[-1])
-    rows, stride = 1, 0
+    shape = t.shape
+    n = len(shape)
+    if n != lead + 1 and n != lead + 2:
+        raise ValueError("the tensor must be [*positions.shape, heads, width] or [*positions.shape, width]")
+    heads = shape[-2] if n == lead + 2 else 1
+    if t.is_contiguous():
+        row = heads * shape[-1]
+        return (t.numel() // row if row else 0), row, heads, shape[-1]
+    strides = t.stride()
+    if strides[-1] != 1:
+        raise ValueError("the tensor's last dimension must be contiguous")
+    rows, row = 1, 0
     for d in reversed(range(lead)):
-        if t.shape[d] == 1:
+        if shape[d] == 1:
             continue
         if rows == 1:
-            stride = t.stride(d)
-        elif t.stride(d) != stride * rows:
+            row = strides[d]
+        elif strides[d] != row * rows:
             raise ValueError("the leading dimensions must fold into one")
-        rows *= t.shape[d]
-    return rows, stride, heads, head_stride
+        rows *= shape[d]
+    return rows, row, heads, strides[-2] if n == lead + 2 else shape[-1]
 
 
 def mla_rope(x, positions, rope, offset=None, out=None, inverse=False, stream=None):
@@ -366,20 +381,21 @@ def mla_rope(x, positions, rope, offset=None, out=None, inverse=False, stream=No
     x = d out, the gradient). `rope` comes from make_rope."""
     _expect(x, "x", torch.bfloat16)
     _expect(positions, "positions", torch.int32)
+    shape, device = x.shape, x.device
     lead = positions.dim()
     rows, x_row, heads, x_head = _rows_and_heads(x, lead)
-    if x.shape[:lead] != positions.shape:
-        raise ValueError(f"x {tuple(x.shape)} does not start with the shape of positions {tuple(positions.shape)}")
+    if shape[:lead] != positions.shape:
+        raise ValueError(f"x {tuple(shape)} does not start with the shape of positions {tuple(positions.shape)}")
+    used = ()
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
         used = (out,)
-    else:
-        _expect(out, "out", torch.bfloat16, tuple(x.shape))
-        used = ()
-    _same_device(x.device, positions=positions, out=out)
+    elif out is not x:
+        _expect(out, "out", torch.bfloat16, shape)
+    _same_device(device, positions, out)
     _, o_row, _, o_head = _rows_and_heads(out, lead)
-    width = x.shape[-1]
-    _call("mla_rope", x.device, stream,
+    width = shape[-1]
+    _call("mla_rope", device, stream,
           (ctypes.byref(rope), x.data_ptr(), x_row, x_head, out.data_ptr(), o_row, o_head, rows, heads, width,
            width - D_ROPE if offset is None else int(offset), _ptr(positions), 1 if inverse else 0), used)
     return out
@@ -394,25 +410,25 @@ def mla_cache_append(kv_a, norm_weight, positions, rope, kv_cache, k_pe_cache, s
     _expect(positions, "positions", torch.int32)
     _expect(kv_cache, "kv_cache", torch.bfloat16)
     _expect(k_pe_cache, "k_pe_cache", torch.bfloat16)
-    if norm_weight.dtype not in (torch.bfloat16, torch.float32) or tuple(norm_weight.shape) != (D_LATENT,):
+    f32 = norm_weight.dtype == torch.float32
+    if not (f32 or norm_weight.dtype == torch.bfloat16) or norm_weight.shape != (D_LATENT,):
         raise ValueError("norm_weight must be bf16 or float32 [512]")
-    if kv_a.shape != (*positions.shape, D_LATENT + D_ROPE):
+    if kv_a.shape[:-1] != positions.shape or kv_a.shape[-1] != D_LATENT + D_ROPE:
         raise ValueError("kv_a must be [*positions.shape, 576]")
     rows, stride, _, _ = _rows_and_heads(kv_a, positions.dim())
     if rows <= 1:
         stride = D_LATENT + D_ROPE
     if slots is not None:
-        _expect(slots, "slots", torch.int32, tuple(positions.shape))
-    if kv_cache.shape[-1] != D_LATENT or k_pe_cache.shape != (*kv_cache.shape[:-1], D_ROPE):
+        _expect(slots, "slots", torch.int32, positions.shape)
+    if kv_cache.shape[-1] != D_LATENT or k_pe_cache.shape[-1] != D_ROPE or kv_cache.shape[:-1] != k_pe_cache.shape[:-1]:
         raise ValueError("kv_cache must be [..., 512] and k_pe_cache [..., 64] over the same rows")
     cache_rows = kv_cache.numel() // D_LATENT
     if slots is None and cache_rows < rows:
         raise ValueError("the cache has fewer rows than there are tokens")
-    _same_device(kv_a.device, norm_weight=norm_weight, positions=positions, slots=slots, kv_cache=kv_cache,
-                 k_pe_cache=k_pe_cache)
-    _call("mla_cache_append", kv_a.device, stream,
-          (ctypes.byref(rope), kv_a.data_ptr(), stride, _ptr(norm_weight),
-           1 if norm_weight.dtype == torch.float32 else 0, float(eps), _ptr(positions), _ptr(slots), rows,
+    device = kv_a.device
+    _same_device(device, norm_weight, positions, slots, kv_cache, k_pe_cache)
+    _call("mla_cache_append", device, stream,
+          (ctypes.byref(rope), kv_a.data_ptr(), stride, _ptr(norm_weight), 1 if f32 else 0, float(eps), _ptr(positions), _ptr(slots), rows,
            _ptr(kv_cache), _ptr(k_pe_cache), cache_rows))
     return kv_cache, k_pe_cache
 
@@ -424,7 +440,7 @@ def _pages(kv_cache, k_pe_cache, table_width, one_layer):
     if len(shape) not in ((3,) if one_layer else (3, 4)) or shape[-1] != D_LATENT:
         raise ValueError("kv_cache must be [pages, page_size, 512]" +
                          ("" if one_layer else " or [layers, pages, page_size, 512]"))
-    if k_pe_cache.shape != (*shape[:-1], D_ROPE):
+    if k_pe_cache.shape[-1] != D_ROPE or k_pe_cache.shape[:-1] != shape[:-1]:
         raise ValueError("k_pe_cache must be [..., 64] over kv_cache's pages")
     return MlaPages(shape[-3], shape[-2], table_width, shape[0] if len(shape) == 4 else 1)
 
@@ -451,7 +467,7 @@ def mla_tree_decode(q, kv_cache, k_pe_cache, block_table, cache_len, W_kvb, W_o,
     fp8 = _wtype(W_kvb)
     if _wtype(W_o) != fp8:
         raise ValueError("W_kvb and W_o must use the same storage type")
-    if tuple(W_kvb.shape) != (H * (D_NOPE + D_V), D_LATENT) or tuple(W_o.shape) != (H * D_V, D_MODEL):
+    if W_kvb.shape != (H * (D_NOPE + D_V), D_LATENT) or W_o.shape != (H * D_V, D_MODEL):
         raise ValueError("W_kvb must be [H*256, 512] and W_o [H*128, 7168]")
     if fp8:
         for w, s, name in ((W_kvb, W_kvb_scale, "W_kvb_scale"), (W_o, W_o_scale, "W_o_scale")):
@@ -459,9 +475,8 @@ def mla_tree_decode(q, kv_cache, k_pe_cache, block_table, cache_len, W_kvb, W_o,
                 raise ValueError(f"e4m3 weights need {name}")
             _expect(s, name, torch.float32, (w.shape[0] // 128, w.shape[1] // 128))
     pages = _pages(kv_cache, k_pe_cache, block_table.shape[1], True)
-    _same_device(q.device, kv_cache=kv_cache, k_pe_cache=k_pe_cache, block_table=block_table, cache_len=cache_len,
-                 W_kvb=W_kvb, W_o=W_o, W_kvb_scale=W_kvb_scale, W_o_scale=W_o_scale, parents=parents,
-                 n_nodes=n_nodes, out=out, workspace=workspace)
+    _same_device(q.device, kv_cache, k_pe_cache, block_table, cache_len, W_kvb, W_o, W_kvb_scale, W_o_scale, parents,
+                 n_nodes, out, workspace)
     dims = make_dims(B, N, H, 0, fp8)
     used = []
     if out is None:
@@ -493,8 +508,7 @@ def mla_cache_compact(kv_cache, k_pe_cache, block_table, cache_len, accepted, n_
     _expect(cache_len, "cache_len", torch.int32, (B,))
     _expect(accepted, "accepted", torch.int32, (B, accepted.shape[1]))
     _expect(n_accepted, "n_accepted", torch.int32, (B,))
-    _same_device(kv_cache.device, k_pe_cache=k_pe_cache, block_table=block_table, cache_len=cache_len,
-                 accepted=accepted, n_accepted=n_accepted)
+    _same_device(kv_cache.device, k_pe_cache, block_table, cache_len, accepted, n_accepted)
     _call("mla_cache_compact", kv_cache.device, stream,
           (ctypes.byref(pages), _ptr(kv_cache), _ptr(k_pe_cache), _ptr(block_table), _ptr(cache_len), _ptr(accepted),
            _ptr(n_accepted), B, accepted.shape[1]))
@@ -515,7 +529,7 @@ def mla_cache_copy_pages(kv_cache, k_pe_cache, src, dst, stream=None):
             v = v.tolist()
         lists.append(array.array("i", v))  # OverflowError for an index beyond 32 bits
     pages = _pages(kv_cache, k_pe_cache, 0, False)
-    _same_device(kv_cache.device, k_pe_cache=k_pe_cache)
+    _same_device(kv_cache.device, k_pe_cache)
     _call("mla_cache_copy_pages", kv_cache.device, stream,
           (ctypes.byref(pages), _ptr(kv_cache), _ptr(k_pe_cache), lists[0].buffer_info()[0], lists[1].buffer_info()[0], n))
 
