@@ -308,6 +308,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrival
   tc_fence_after();
+  griddep_launch();
   work.base = start[0];
   work.b = static_cast<int>(start[1]);
   const uint32_t tmem = *tmem_slot;
@@ -372,6 +373,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
     };
     bool ok = true;
     int g = 0, runs = 0;  // blocks and runs so far
+    griddep_wait();       // q_abs; what comes before it here reads only what was there before that kernel began
     if (warp == 0) {
       const uint32_t rope0 = smem_u32(smem + S::ROPE), empty0 = bar(kTreeEmpty), rfull0 = bar(kTreeRopeFull);
       const uint32_t kfull0_leader = mapa_shared(kfull0, 0), rfull0_leader = mapa_shared(rfull0, 0);
@@ -770,6 +772,8 @@ __global__ void __launch_bounds__(kTreeJoinThreads)
 tree_combine_kernel(const TreeParams p, int pairs) {
   __shared__ int slots[96];
   __shared__ int found[3];
+  griddep_launch();
+  griddep_wait();
   const int all_tiles = (p.N * p.H + kTreeRows - 1) / kTreeRows;
   const int at = static_cast<int>(blockIdx.x) / kTreeJoinBlocks, b = at / all_tiles, tile = at % all_tiles;
   const int item = static_cast<int>(blockIdx.x) % kTreeJoinBlocks * kTreeJoinThreads + static_cast<int>(threadIdx.x);

@@ -165,6 +165,7 @@ gemm_m64_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const Abort ab{abort_word, err};
+  griddep_launch();
 
   // K, N multiples of BK, BN (host-checked)
   M64Work work(M, N, K, bt.count, Cfg::BM, Cfg::BATCH);
@@ -172,7 +173,8 @@ gemm_m64_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
   if (warp == 0) {
     if (lane == 0) {
-      // ---------------- TMA producer
+      // ---------------- TMA producer (everything else follows from its loads)
+      griddep_wait();
       int it = 0;
       bool ok = true;
       while (ok && work.next(sg)) {
@@ -300,6 +302,8 @@ sum_segments_kernel(const float* __restrict__ part, int M, int N, int K, int bm,
                     __nv_bfloat16* __restrict__ out, int* err) {
   __shared__ int parts[kSumMaxParts];
   __shared__ int nparts;
+  griddep_launch();
+  griddep_wait();
   const int num_m = (M + bm - 1) / bm, nkb = K / 64;
   const int chunks = bm / kSumRows;
   const int t = blockIdx.x / chunks, r0 = (blockIdx.x % chunks) * kSumRows;

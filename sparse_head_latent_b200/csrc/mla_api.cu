@@ -277,6 +277,35 @@ int timed_launch(int cls, cudaStream_t stream, F&& launch) {
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
+// Launch of a kernel on `st`, as a dependent of the one before it if asked for
+// (see griddep_wait): then that one must call griddep_launch, the kernel must
+// call griddep_wait before it touches anything the chain's kernels write, and the
+// chain must begin with a plain launch.
+template <class... P, class... A>
+cudaError_t launch_kernel(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+                          bool dependent, unsigned cluster, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (dependent) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 }  // namespace
 
 // ------------------------------------------------------------------ validation and workspace
@@ -695,17 +724,20 @@ int launch_gemm8_wo(const DeviceState* ds, int M, int H, const void* attn8, cons
 // split of one GEMM over `grid` CTAs.
 template <class Cfg64, class Cfg128>
 int launch_m64(const DeviceState* ds, const CUtensorMap& ta, const CUtensorMap& tb, int M, int N, int K,
-               const mla::M64Batch& bt, int grid, float* part, void* out, int cls, cudaStream_t st) {
+               const mla::M64Batch& bt, int grid, float* part, void* out, int cls, cudaStream_t st,
+               bool dependent = false) {
   const int bm = M <= 64 ? 64 : 128;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
-  return timed_launch(cls, st, [&] {
+  cudaError_t le = cudaSuccess;
+  const int rc = timed_launch(cls, st, [&] {
     if (bm == 64)
-      mla::gemm_m64_kernel<Cfg64><<<grid, Cfg64::THREADS, Cfg64::SMEM_BYTES, st>>>(ta, tb, M, N, K, bt, part,
-                                                                                         o, ds->err);
+      le = launch_kernel(mla::gemm_m64_kernel<Cfg64>, grid, Cfg64::THREADS, Cfg64::SMEM_BYTES, st, dependent, 1, ta, tb,
+                         M, N, K, bt, part, o, ds->err);
     else
-      mla::gemm_m64_kernel<Cfg128><<<grid, Cfg128::THREADS, Cfg128::SMEM_BYTES, st>>>(ta, tb, M, N, K, bt,
-                                                                                            part, o, ds->err);
+      le = launch_kernel(mla::gemm_m64_kernel<Cfg128>, grid, Cfg128::THREADS, Cfg128::SMEM_BYTES, st, dependent, 1, ta,
+                         tb, M, N, K, bt, part, o, ds->err);
   });
+  return le != cudaSuccess ? MLA_ERR_CUDA : rc;
 }
 
 // Output projection of M <= 256 rows as a stream-K GEMM (M = 64 or 128 UMMA
@@ -713,7 +745,7 @@ int launch_m64(const DeviceState* ds, const CUtensorMap& ta, const CUtensorMap& 
 // one fp32 partial tile per tile it touches into `part` (room for
 // kStreamKCtas + tiles of them); a second kernel sums them into `out`.
 int launch_gemm_wo_m64(const DeviceState* ds, int M, int H, const void* attn, const void* wo, float* part,
-                       void* out, cudaStream_t st) {
+                       void* out, cudaStream_t st, bool dependent = false) {
   const int N = kD, K = H * kDv;
   const int bm = M <= 64 ? 64 : 128;
   CUtensorMap ta, tb;
@@ -724,13 +756,15 @@ int launch_gemm_wo_m64(const DeviceState* ds, int M, int H, const void* attn, co
   int grid = ds->sms < kStreamKCtas ? ds->sms : kStreamKCtas;
   if (units < grid) grid = static_cast<int>(units);
   const mla::M64Batch bt = {1, 0, 0, 0, 0, 0};
-  int rc = launch_m64<GemmM64, GemmM128>(ds, ta, tb, M, N, K, bt, grid, part, nullptr, 4, st);
+  int rc = launch_m64<GemmM64, GemmM128>(ds, ta, tb, M, N, K, bt, grid, part, nullptr, 4, st, dependent);
   if (rc != MLA_OK) return rc;
   const int blocks = ((M + bm - 1) / bm) * (N / GemmM64::BN) * (bm / mla::kSumRows);
-  return timed_launch(4, st, [&] {
-    mla::sum_segments_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(part, M, N, K, bm, grid,
-                                                                            static_cast<__nv_bfloat16*>(out), ds->err);
+  cudaError_t le = cudaSuccess;
+  rc = timed_launch(4, st, [&] {
+    le = launch_kernel(mla::sum_segments_kernel, blocks, 256, 0, st, dependent, 1, part, M, N, K, bm, grid,
+                       static_cast<__nv_bfloat16*>(out), ds->err);
   });
+  return le != cudaSuccess ? MLA_ERR_CUDA : rc;
 }
 
 int launch_prepass(const DeviceState* ds, const mla_dims& d, const int32_t* topk, void* bitmap, void* blocks,
@@ -853,7 +887,7 @@ int launch_gemm_absorb(const DeviceState* ds, int H, int rows, const void* q_row
 // attn[r, h, :] = o_lat[r, h, :] . W_kvb[h*256 + 128 + (0..127), :]^T: one
 // GEMM per head (M = rows, N = 128, K = 512).
 int launch_gemm_unabsorb(const DeviceState* ds, int H, int rows, const void* olat, const void* wk, void* attn_rows,
-                         cudaStream_t st) {
+                         cudaStream_t st, bool dependent = false) {
   CUtensorMap ta, tb, tc;
   if (rows <= kFewRows) {
     if (!map_2d(&ta, olat, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<uint64_t>(H) * kL, rows,
@@ -864,7 +898,7 @@ int launch_gemm_unabsorb(const DeviceState* ds, int H, int rows, const void* ola
     const mla::M64Batch bt = {H, kL, kDn, kDn + kDv, kDv, H * kDv};
     const int items = (rows <= 64 ? 1 : (rows + 127) / 128) * H;
     return launch_m64<GemmM64Unabs, GemmM128Unabs>(ds, ta, tb, rows, kDv, kL, bt, items < ds->sms ? items : ds->sms,
-                                                   nullptr, attn_rows, 6, st);
+                                                   nullptr, attn_rows, 6, st, dependent);
   }
   if (!map_2d(&ta, olat, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<uint64_t>(H) * kL, rows,
               static_cast<uint64_t>(H) * kL * 2, 64, 128) ||
@@ -1109,7 +1143,7 @@ mla::RopeTable rope_table(const mla_rope_table& t) {
 int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pages& pg, const WsLayout& lay, void* ws,
                           const void* q, const void* kv, const void* pe, const int32_t* table,
                           const int32_t* cache_len, const int32_t* n_nodes, const int32_t* parents, float scale,
-                          cudaStream_t st) {
+                          cudaStream_t st, bool dependent) {
   mla::TreeParams p = {};
   p.B = d.B;
   p.N = d.T;
@@ -1136,26 +1170,19 @@ int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pa
       !map_chunks(&tqa, ws_at(ws, lay.qabs), qrows, 64, 2) ||
       !map_2d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDn + kDr, qrows, (kDn + kDr) * 2, 64, 64))
     return MLA_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * ds->pairs_tree), 1, 1);
-  cfg.blockDim = dim3(mla::kTreeThreads, 1, 1);
-  cfg.dynamicSmemBytes = mla::TreeSmem::BYTES;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   cudaError_t le = cudaSuccess;
-  int rc = timed_launch(7, st, [&] { le = cudaLaunchKernelEx(&cfg, mla::tree_attn_kernel, tkv, tpe, tqa, tq, p); });
+  int rc = timed_launch(7, st, [&] {
+    le = launch_kernel(mla::tree_attn_kernel, 2 * ds->pairs_tree, mla::kTreeThreads, mla::TreeSmem::BYTES, st, dependent, 2,
+                       tkv, tpe, tqa, tq, p);
+  });
   if (le != cudaSuccess) return MLA_ERR_CUDA;
   if (rc != MLA_OK) return rc;
   const int64_t join = static_cast<int64_t>(d.B) * ((d.T * d.H + mla::kTreeRows - 1) / mla::kTreeRows) * mla::kTreeJoinBlocks;
-  return timed_launch(7, st, [&] {
-    mla::tree_combine_kernel<<<static_cast<unsigned>(join), mla::kTreeJoinThreads, 0, st>>>(p, ds->pairs_tree);
+  rc = timed_launch(7, st, [&] {
+    le = launch_kernel(mla::tree_combine_kernel, static_cast<unsigned>(join), mla::kTreeJoinThreads, 0, st, dependent, 1, p,
+                       ds->pairs_tree);
   });
+  return le != cudaSuccess ? MLA_ERR_CUDA : rc;
 }
 
 // One decoding step of B trees of N nodes.
@@ -1174,19 +1201,23 @@ int run_tree_decode(const DeviceState* ds, const mla_dims& d, const mla_pages& p
   void* qabs = ws_at(ws, lay.qabs);
   void* olat = ws_at(ws, lay.olat);
   void* attn = ws_at(ws, lay.attn);
-  if ((rc = launch_gemm_absorb(ds, d.H, rows, q, wk, qabs, st)) != MLA_OK) return rc;
-  if ((rc = launch_tree_attention(ds, d, pg, lay, ws, q, kv, pe, table, cache_len, n_nodes, parents, scale, st)) !=
-      MLA_OK)
-    return rc;
-  if ((rc = launch_gemm_unabsorb(ds, d.H, rows, olat, wk, attn, st)) != MLA_OK) return rc;
+  // Few rows: after the first, each kernel is launched as a dependent of the one
+  // before, so that its set-up runs while that one ends. The pair GEMMs of more
+  // rows take plain launches.
+  const bool few = rows <= kFewRows;
   const void* wo = W_o;
   if (d.wdtype == MLA_W_E4M3_BLOCK128) {
     void* dq = ws_at(ws, lay.wo);
     if ((rc = launch_dequant(ds, W_o, W_o_scale, dq, d.H * kDv, kD, st)) != MLA_OK) return rc;
     wo = dq;
   }
+  if ((rc = launch_gemm_absorb(ds, d.H, rows, q, wk, qabs, st)) != MLA_OK) return rc;
+  if ((rc = launch_tree_attention(ds, d, pg, lay, ws, q, kv, pe, table, cache_len, n_nodes, parents, scale, st, few)) !=
+      MLA_OK)
+    return rc;
+  if ((rc = launch_gemm_unabsorb(ds, d.H, rows, olat, wk, attn, st, few)) != MLA_OK) return rc;
   if (lay.wo_part != kNone)
-    return launch_gemm_wo_m64(ds, rows, d.H, attn, wo, reinterpret_cast<float*>(ws_at(ws, lay.wo_part)), out, st);
+    return launch_gemm_wo_m64(ds, rows, d.H, attn, wo, reinterpret_cast<float*>(ws_at(ws, lay.wo_part)), out, st, few);
   return launch_gemm_wo(ds, rows, d.H, attn, wo, out, st);
 }
 
@@ -1519,15 +1550,18 @@ int mla_cache_compact(const mla_pages* pages, void* kv_cache, void* k_pe_cache, 
   p.counts = n_accepted;
   p.width = width;
   p.err = ds->err;
-  const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>(pages->layers));
+  p.layers = pages->layers;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // Rows a thread holds: 2, 4 or 16, by the most that a sequence can accept.
+  // Rows of a layer a thread holds: 2, 4 or 16, by the most that a sequence can
+  // accept; four layers a block unless the rows fill the registers.
+  const int per_block = width <= 4 * mla::kCompactRows ? 4 : 1;
+  const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>((pages->layers + per_block - 1) / per_block));
   if (width <= 2 * mla::kCompactRows)
-    mla::cache_compact_kernel<2><<<grid, mla::kCompactThreads, 0, st>>>(p);
+    mla::cache_compact_kernel<2, 4><<<grid, mla::kCompactThreads, 0, st>>>(p);
   else if (width <= 4 * mla::kCompactRows)
-    mla::cache_compact_kernel<4><<<grid, mla::kCompactThreads, 0, st>>>(p);
+    mla::cache_compact_kernel<4, 4><<<grid, mla::kCompactThreads, 0, st>>>(p);
   else
-    mla::cache_compact_kernel<MLA_MAX_TREE / mla::kCompactRows><<<grid, mla::kCompactThreads, 0, st>>>(p);
+    mla::cache_compact_kernel<MLA_MAX_TREE / mla::kCompactRows, 1><<<grid, mla::kCompactThreads, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

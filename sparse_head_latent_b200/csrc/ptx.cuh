@@ -60,6 +60,14 @@ __device__ __forceinline__ uint32_t lane_id() {
   return l;
 }
 
+// Programmatic dependent launch. A kernel launched as dependent starts while
+// the kernel before it still runs (once all its blocks have said
+// griddep_launch or ended); griddep_wait waits until that kernel, and with it
+// everything before it, has completed and its writes are visible. Without the
+// launch attribute both do nothing.
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

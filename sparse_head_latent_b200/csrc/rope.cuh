@@ -91,19 +91,13 @@ rope_kernel(const __grid_constant__ RopeTable tab, const RopeParams p) {
   if (row >= p.rows) return;
   const int k = piece - p.rope_chunk;  // which of the 8 rotary pieces
   const bool turn = k >= 0 && k < 8;
-  float2 cs[4];
-  if (turn) {
-    const int pos = __ldg(p.positions + row);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = rope_cos_sin(pos, tab.turns[4 * k + i], tab.magnitude, p.inverse);
-  }
   // HALF: the thread of rotary piece k turns pairs 4k .. 4k+3, whose two
   // halves are 8 bytes each at elements 4k and 32 + 4k of the rotary part.
   const int lo = HALF && turn ? p.rope_chunk * 8 + 4 * k : piece * 8;
   const __nv_bfloat16* x = p.x + row * p.x_row + lo;
   __nv_bfloat16* out = p.out + row * p.o_row + lo;
-  for (; h < h_end; h += 4 * h_step) {
-    uint4 w[4];
+  uint4 w[4];
+  auto load = [&]() {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (h + i * h_step >= h_end) break;
@@ -115,6 +109,15 @@ rope_kernel(const __grid_constant__ RopeTable tab, const RopeParams p) {
         w[i] = *reinterpret_cast<const uint4*>(s);
       }
     }
+  };
+  load();  // in flight while the cosines are made
+  float2 cs[4];
+  if (turn) {
+    const int pos = __ldg(p.positions + row);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[i] = rope_cos_sin(pos, tab.turns[4 * k + i], tab.magnitude, p.inverse);
+  }
+  while (h < h_end) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (h + i * h_step >= h_end) break;
@@ -144,6 +147,8 @@ rope_kernel(const __grid_constant__ RopeTable tab, const RopeParams p) {
         *reinterpret_cast<uint4*>(d) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
+    h += 4 * h_step;
+    if (h < h_end) load();
   }
 }
 
@@ -171,15 +176,27 @@ cache_append_kernel(const __grid_constant__ RopeTable tab, const AppendParams p)
   const int lane = threadIdx.x & 31;
   const int row = static_cast<int>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (row >= p.rows) return;
+  // Everything is loaded before anything is looked at.
   const int64_t slot = p.slots ? __ldg(p.slots + row) : row;
   const int pos = __ldg(p.positions + row);
-  if (slot < 0 || slot >= p.cache_rows) return;
   const __nv_bfloat16* src = p.kv_a + row * p.kv_row;
-  uint4 w[2];
+  uint4 w[2], gw[4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + lane + 32 * i);
   const __nv_bfloat16* key = src + 512 + (HALF ? lane : 2 * lane);
-  const float u = __bfloat162float(key[0]), v = __bfloat162float(key[HALF ? 32 : 1]);
+  const __nv_bfloat16 ku = key[0], kv = key[HALF ? 32 : 1];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (p.weight_f32) {
+      const uint4* wf = static_cast<const uint4*>(p.weight) + 2 * (lane + 32 * i);
+      gw[2 * i] = __ldg(wf);
+      gw[2 * i + 1] = __ldg(wf + 1);
+    } else {
+      gw[2 * i] = __ldg(static_cast<const uint4*>(p.weight) + lane + 32 * i);
+    }
+  }
+  if (slot < 0 || slot >= p.cache_rows) return;
+  const float u = __bfloat162float(ku), v = __bfloat162float(kv);
   float x[16];
   float sum = 0.f;
 #pragma unroll
@@ -201,12 +218,12 @@ cache_append_kernel(const __grid_constant__ RopeTable tab, const AppendParams p)
   for (int i = 0; i < 2; ++i) {
     float g[8];
     if (p.weight_f32) {
-      const float4* wf = static_cast<const float4*>(p.weight) + 2 * (lane + 32 * i);
-      const float4 a = __ldg(wf), b = __ldg(wf + 1);
-      g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w, g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+      const uint32_t in[8] = {gw[2 * i].x,     gw[2 * i].y,     gw[2 * i].z,     gw[2 * i].w,
+                              gw[2 * i + 1].x, gw[2 * i + 1].y, gw[2 * i + 1].z, gw[2 * i + 1].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = __uint_as_float(in[e]);
     } else {
-      const uint4 a = __ldg(static_cast<const uint4*>(p.weight) + lane + 32 * i);
-      const uint32_t in[4] = {a.x, a.y, a.z, a.w};
+      const uint32_t in[4] = {gw[2 * i].x, gw[2 * i].y, gw[2 * i].z, gw[2 * i].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 f = bf16x2_float2(in[e]);
