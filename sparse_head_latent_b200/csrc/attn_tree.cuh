@@ -66,6 +66,7 @@ struct TreeParams {
   const int32_t* cache_len;      // [B]
   const int32_t* n_nodes;        // [B], or nullptr: N each
   const int32_t* parents;        // [B][N], or nullptr: a chain
+  const float* v_scale;          // [2 H][4], or nullptr: row 2 h + 1 multiplies the four 128s of head h's o_lat
   __nv_bfloat16* olat;           // [B*N][H][512]
   int64_t* ustart;               // [B + 1] first unit of each sequence, and their number
   float* part_o;                 // [2 pairs][128 value quads][128 rows][4] unnormalised partial tiles
@@ -714,7 +715,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       const float l = (all[0] + all[1]) + (all[2] + all[3]);
       const int v0 = 256 * ch + 128 * lh;  // this thread's 128 of the 512 values
       if (sg_done.j1 - sg_done.j0 == sg_done.blocks) {
-        const float inv = l != 0.f ? 1.f / l : 0.f;
+        float inv = l != 0.f ? 1.f / l : 0.f;
+        if (p.v_scale != nullptr) inv *= __ldg(p.v_scale + (2 * (r % p.H) + 1) * 4 + (v0 >> 7));
         uint4* dst = reinterpret_cast<uint4*>(p.olat + ((static_cast<int64_t>(sg_done.b) * p.N) * p.H + r) * 512 + v0);
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += 32) {
@@ -831,7 +833,8 @@ tree_combine_kernel(const TreeParams p, int pairs) {
       acc[4 * k + 3] = fmaf(w, v[k].w, acc[4 * k + 3]);
     }
   }
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  float inv = sum != 0.f ? 1.f / sum : 0.f;
+  if (p.v_scale != nullptr) inv *= __ldg(p.v_scale + (2 * (r % p.H) + 1) * 4 + (v0 >> 7));
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     dst[i] = make_uint4(pack_bf16x2(acc[8 * i] * inv, acc[8 * i + 1] * inv),

@@ -1,0 +1,285 @@
+// gemm_m64_w8.cuh -- the few-row GEMM (gemm_m64.cuh) over e4m3 weights read as
+// they are stored, for mla_tree_decode on sm_100a.
+//
+// mla_decode first writes a bf16 copy of W_kvb and W_o: the 134 MB of codes of
+// 128 heads are read, 268 MB written and read again, 89 us before the products
+// begin. Here each CTA's share of the codes goes from HBM to shared memory by
+// TMA and eight warps turn it into the bf16 operand there, so that a weight
+// costs one byte of HBM traffic. Scales (one per 128 x 128 block):
+//   absorb  (q_nope . W_UK, K = 128): one scale per output tile, applied to the
+//           fp32 accumulator; the codes are exact in bf16
+//   unabsorb (o_lat . W_UV^T, K = 512): one scale per 128 of K, which the
+//           attention has multiplied into o_lat before rounding it
+//   W_o     (stream-K): bf16(code * scale), rounded once, as the copy would be
+//
+// Roles (448 threads, one CTA per SM): warp 0 TMA producer; warp 1 tensor memory
+// and UMMA issuer; warps 2..5 epilogue; warps 6..13 converters. A stage holds A
+// [BM x 64] and the codes of [64 x 128] weights (8 KB); three 16 KB buffers hold
+// converted operands. Work (segments, stream-K shares, batches) as in
+// gemm_m64.cuh.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "gemm_m64.cuh"
+
+namespace mla {
+
+// B_MN_MAJOR_: weights stored [K, N]; else [N, K]. BATCH_: one product per head
+// with bf16 C; else stream-K with fp32 partial tiles and scaled conversion.
+template <int BM_, bool B_MN_MAJOR_, bool BATCH_>
+struct GemmM64W8Cfg {
+  static constexpr int BM = BM_, BN = 128, BK = 64;
+  static constexpr bool B_MN_MAJOR = B_MN_MAJOR_, BATCH = BATCH_;
+  static constexpr int STAGES = BM_ == 64 ? 10 : 7;
+  static constexpr int A_BYTES = BM * BK * 2, W_BYTES = BK * BN;
+  static constexpr int STAGE_BYTES = A_BYTES + W_BYTES;
+  static constexpr int BUFS = 3, BUF_BYTES = BK * BN * 2;
+  static constexpr int CONVERTERS = 8;
+  static constexpr int THREADS = 192 + 32 * CONVERTERS;
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * BUFS + 4;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + BUFS * BUF_BYTES + NUM_BARS * 8 + 16;
+  static constexpr uint32_t TMEM_COLS = 256;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+// Two e4m3 codes to two bf16, times s if SCALED (fp32 product, one rounding;
+// without it exact).
+template <bool SCALED>
+__device__ __forceinline__ uint32_t e4m3x2_bf16x2(uint32_t codes, float s) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xffffu), __NV_E4M3);
+  float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  if (SCALED) f.x *= s, f.y *= s;
+  return pack_bf16x2(f.x, f.y);
+}
+
+// scale: BATCH and B_MN_MAJOR (absorb): [2 * count][4], entry (2 z) * 4 + nt for
+// the accumulator of item z, column tile nt; stream-K: [K / 128][N / 128];
+// BATCH and K-major: unused.
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, int M, int N, int K,
+                   const M64Batch bt, const float* __restrict__ scale, float* __restrict__ part,
+                   __nv_bfloat16* __restrict__ out, int* err) {
+  constexpr int BK = Cfg::BK, S = Cfg::STAGES, NB = Cfg::BUFS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* bufs = smem + S * Cfg::STAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(bufs + NB * Cfg::BUF_BYTES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
+  int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S;
+  const uint32_t bfull0 = empty0 + 8 * S, bempty0 = bfull0 + 8 * NB;
+  const uint32_t accf0 = bempty0 + 8 * NB, acce0 = accf0 + 16;
+  const int warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < NB; ++b) {
+      mbar_init(bfull0 + 8 * b, Cfg::CONVERTERS);
+      mbar_init(bempty0 + 8 * b, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(accf0 + 8 * a, 1);
+      mbar_init(acce0 + 8 * a, 4);  // the four epilogue warps
+    }
+    *abort_word = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), Cfg::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const Abort ab{abort_word, err};
+  griddep_launch();
+
+  M64Work work(M, N, K, bt.count, Cfg::BM, Cfg::BATCH);
+  M64Seg sg;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer. The weights do not come from the kernel
+      // before this one: the first stages' codes are asked for at once, A after it.
+      int it = 0, asked = 0;
+      bool ok = true;
+      {
+        M64Work ahead = work;
+        M64Seg a;
+        while (asked < S && ahead.next(a)) {
+          for (int kb = a.kb0; kb < a.kb1 && asked < S; ++kb, ++asked) {
+            mbar_arrive_expect_tx(full0 + 8 * asked, Cfg::STAGE_BYTES);
+            const uint32_t w = smem_u32(smem + asked * Cfg::STAGE_BYTES) + Cfg::A_BYTES;
+            const int r = bt.b_row0 + a.z * bt.b_step;
+            if constexpr (Cfg::B_MN_MAJOR)
+              tma_load_2d(w, &tmW, full0 + 8 * asked, a.nt * Cfg::BN, r + kb * BK);
+            else
+              tma_load_2d(w, &tmW, full0 + 8 * asked, kb * BK, r + a.nt * Cfg::BN);
+          }
+        }
+      }
+      griddep_wait();
+      while (ok && work.next(sg)) {
+        for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
+          const int s = it % S;
+          const uint32_t fb = full0 + 8 * s;
+          const uint32_t sa = smem_u32(smem + s * Cfg::STAGE_BYTES);
+          const int k = kb * BK;
+          if (it >= asked) {
+            if (!mbar_wait(empty0 + 8 * s, ((it / S) & 1) ^ 1, ab, kErrWaitConsumer)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(fb, Cfg::STAGE_BYTES);
+            const int r = bt.b_row0 + sg.z * bt.b_step;
+            if constexpr (Cfg::B_MN_MAJOR)
+              tma_load_2d(sa + Cfg::A_BYTES, &tmW, fb, sg.nt * Cfg::BN, r + k);
+            else
+              tma_load_2d(sa + Cfg::A_BYTES, &tmW, fb, k, r + sg.nt * Cfg::BN);
+          }
+          tma_load_2d(sa, &tmA, fb, sg.z * bt.a_step + k, sg.mt * Cfg::BM);  // rows past M read as zero
+        }
+      }
+      if (!ok) spin_ns(2000000);  // let issued loads land before the CTA can exit
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------- UMMA issuer
+      constexpr uint32_t idesc = idesc_bf16_f32(Cfg::BM, Cfg::BN, 0, Cfg::B_MN_MAJOR ? 1 : 0);
+      int it = 0, t = 0;
+      bool ok = true;
+      for (; ok && work.next(sg); ++t) {
+        const int a = t & 1;
+        if (!mbar_wait(acce0 + 8 * a, ((t >> 1) & 1) ^ 1, ab, kErrWaitEpilogue)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + a * Cfg::BN;
+        for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
+          const int s = it % S, b = it % NB;
+          if (!mbar_wait(full0 + 8 * s, (it / S) & 1, ab, kErrWaitTma) ||
+              !mbar_wait(bfull0 + 8 * b, (it / NB) & 1, ab, kErrWaitSoftmax)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + s * Cfg::STAGE_BYTES), sb = smem_u32(bufs + b * Cfg::BUF_BYTES);
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k)
+            umma_ss(d, smem_desc_sw128(sa + k * 32, 16, 1024),
+                    Cfg::B_MN_MAJOR ? smem_desc_sw128(sb + k * 16 * 128, BK * 128, 1024)
+                                    : smem_desc_sw128(sb + k * 32, 16, 1024),
+                    idesc, (kb != sg.kb0 || k != 0) ? 1u : 0u);
+          umma_commit(empty0 + 8 * s);
+          umma_commit(bempty0 + 8 * b);
+        }
+        if (!ok) break;
+        umma_commit(accf0 + 8 * a);
+      }
+      if (!ok && it > 0) {
+        const int i = it - 1;
+        mbar_wait_drain(empty0 + 8 * (i % S), (i / S) & 1);
+      }
+    }
+  } else if (warp >= 6) {
+    // ---------------- converters: 16 codes at a time, 512 such pieces per stage.
+    // A row of 64 codes (64 bytes, four pieces) becomes a 128-byte operand row:
+    // stored [K, N], code row k holds two, of the 64-column chunks 0 and 1;
+    // stored [N, K], one. Lanes take neighbouring pieces: loads and both
+    // stores are free of bank conflicts.
+    const int me = static_cast<int>(threadIdx.x) - 192;
+    int it = 0;
+    bool ok = true;
+    while (ok && work.next(sg)) {
+      for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
+        const int s = it % S, b = it % NB;
+        float f = 1.f;
+        if constexpr (!Cfg::BATCH) f = __ldg(scale + static_cast<int64_t>(kb >> 1) * (N / 128) + sg.nt);
+        if (!(ok = warp_wait_all(bempty0 + 8 * b, ((it / NB) & 1) ^ 1, ab, kErrWaitMma) &&
+                   warp_wait_all(full0 + 8 * s, (it / S) & 1, ab, kErrWaitTma)))
+          break;
+        const uint8_t* src = smem + s * Cfg::STAGE_BYTES + Cfg::A_BYTES;
+        uint8_t* dst = bufs + b * Cfg::BUF_BYTES;
+#pragma unroll
+        for (int i = 0; i < 512 / (32 * Cfg::CONVERTERS); ++i) {
+          const int piece = me + i * 32 * Cfg::CONVERTERS, row64 = piece >> 2, q = piece & 3;
+          const uint4 w = *reinterpret_cast<const uint4*>(src + piece * 16);
+          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[2 * e] = e4m3x2_bf16x2<!Cfg::BATCH>(in[e], f);
+            o[2 * e + 1] = e4m3x2_bf16x2<!Cfg::BATCH>(in[e] >> 16, f);
+          }
+          const int r = Cfg::B_MN_MAJOR ? row64 >> 1 : row64;
+          uint8_t* d = dst + (Cfg::B_MN_MAJOR ? (row64 & 1) * BK * 128 : 0) + r * 128;
+          *reinterpret_cast<uint4*>(d + (((2 * q) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(d + (((2 * q + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bfull0 + 8 * b);
+      }
+    }
+  } else {
+    // ---------------- epilogue: rows [16q, 16q+16) of the tile in lanes 0..15
+    // (M = 64) or [32q, 32q+32) in all lanes (M = 128)
+    constexpr int RPW = Cfg::BM / 4;  // rows per warp
+    const int q = warp & 3;
+    int t = 0;
+    for (; work.next(sg); ++t) {
+      const int a = t & 1;
+      float f = 1.f;
+      if constexpr (Cfg::BATCH && Cfg::B_MN_MAJOR) f = __ldg(scale + 8 * sg.z + sg.nt);
+      if (!warp_wait(accf0 + 8 * a, (t >> 1) & 1, ab, kErrWaitMma)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + a * Cfg::BN;
+      const int row = sg.mt * Cfg::BM + RPW * q + static_cast<int>(lane);
+#pragma unroll 1
+      for (int c = 0; c < Cfg::BN; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tb + c, v);
+        if (static_cast<int>(lane) < RPW && row < M) {
+          if constexpr (Cfg::BATCH) {
+            uint4* d4 = reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * bt.ldc + sg.z * bt.c_step +
+                                                 sg.nt * Cfg::BN + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[e] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * e]) * f, __uint_as_float(v[8 * i + 2 * e + 1]) * f);
+              d4[i] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          } else {
+            float4* d4 = reinterpret_cast<float4*>(
+                part + (static_cast<size_t>(sg.slot) * Cfg::BM + (row - sg.mt * Cfg::BM)) * Cfg::BN + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              d4[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                  __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acce0 + 8 * a);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+}
+
+}  // namespace mla

@@ -22,6 +22,7 @@
 #include "gemm_w8t.cuh"
 #include "gemm8.cuh"
 #include "gemm_m64.cuh"
+#include "gemm_m64_w8.cuh"
 #include "pages.cuh"
 #include "prepass.cuh"
 #include "quant.cuh"
@@ -48,6 +49,12 @@ using GemmM64Abs = mla::GemmM64Cfg<64, true, true>;     // decode's q_nope x W_U
 using GemmM128Abs = mla::GemmM64Cfg<128, true, true>;
 using GemmM64Unabs = mla::GemmM64Cfg<64, false, true>;  // decode's o_lat x W_UV^T per head, bf16 out
 using GemmM128Unabs = mla::GemmM64Cfg<128, false, true>;
+using GemmW8Wo64 = mla::GemmM64W8Cfg<64, true, false>;      // the same three over e4m3 codes (tree decode)
+using GemmW8Wo128 = mla::GemmM64W8Cfg<128, true, false>;
+using GemmW8Abs64 = mla::GemmM64W8Cfg<64, true, true>;
+using GemmW8Abs128 = mla::GemmM64W8Cfg<128, true, true>;
+using GemmW8Unabs64 = mla::GemmM64W8Cfg<64, false, true>;
+using GemmW8Unabs128 = mla::GemmM64W8Cfg<128, false, true>;
 using Gemm8Kvb = mla::Gemm8Cfg<false>;              // e4m3 latent x e4m3 W_kvb^T
 using Gemm8KvbAttn = mla::Gemm8Cfg<false, true>;    // same, v tiles written as f16 for the attention
 using Gemm8Wo = mla::Gemm8Cfg<true>;           // e4m3 attn x e4m3 W_o (B stored [K, N])
@@ -165,6 +172,15 @@ int device_state(DeviceState** out) {
                                       GemmM128Unabs::SMEM_BYTES) == cudaSuccess;
       ok = ok && cudaFuncSetAttribute(mla::absorbed_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       mla::AbsSmem::BYTES) == cudaSuccess;
+      auto w8_smem = [](auto kernel, int bytes) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+      };
+      ok = ok && w8_smem(mla::gemm_m64_w8_kernel<GemmW8Wo64>, GemmW8Wo64::SMEM_BYTES) &&
+           w8_smem(mla::gemm_m64_w8_kernel<GemmW8Wo128>, GemmW8Wo128::SMEM_BYTES) &&
+           w8_smem(mla::gemm_m64_w8_kernel<GemmW8Abs64>, GemmW8Abs64::SMEM_BYTES) &&
+           w8_smem(mla::gemm_m64_w8_kernel<GemmW8Abs128>, GemmW8Abs128::SMEM_BYTES) &&
+           w8_smem(mla::gemm_m64_w8_kernel<GemmW8Unabs64>, GemmW8Unabs64::SMEM_BYTES) &&
+           w8_smem(mla::gemm_m64_w8_kernel<GemmW8Unabs128>, GemmW8Unabs128::SMEM_BYTES);
       ok = ok && cudaFuncSetAttribute(mla::tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       mla::TreeSmem::BYTES) == cudaSuccess;
       if (ok) {
@@ -464,7 +480,8 @@ WsLayout ws_layout(const mla_dims& d, int entry, bool has_topk) {
       w.wo_part = take((kStreamKCtas + tiles) * bm * 128 * 4);
     }
   }
-  const bool dec = entry == MLA_ENTRY_DECODE || entry == MLA_ENTRY_TREE_DECODE;
+  // Decoding reads bf16 copies of e4m3 weights; trees of few rows the codes.
+  const bool copies = entry == MLA_ENTRY_DECODE || (entry == MLA_ENTRY_TREE_DECODE && rows > kFewRows);
   const bool act8 = d.act == MLA_ACT_E4M3_DYNAMIC;
   if (act8) {
     if (attend || entry == MLA_ENTRY_KV_UPPROJECT) {
@@ -482,14 +499,14 @@ WsLayout ws_layout(const mla_dims& d, int entry, bool has_topk) {
         static_cast<int>(H * kDv / 64) >= kSplitMinTileKb)
       w.wo_split = take(static_cast<size_t>(kSplitSlots) * mla::SPLIT_SLOT_FLOATS * 4);
     if (!g_e4m3_onchip) {
-      if (fp8 && (attend || dec || entry == MLA_ENTRY_KV_UPPROJECT)) w.wkvb = take(H * (kDn + kDv) * kL * 2);
-      if (fp8 && (entry == MLA_ENTRY_PREFILL || dec || entry == MLA_ENTRY_OUT_PROJECT)) w.wo = take(H * kDv * kD * 2);
+      if (fp8 && (attend || copies || entry == MLA_ENTRY_KV_UPPROJECT)) w.wkvb = take(H * (kDn + kDv) * kL * 2);
+      if (fp8 && (entry == MLA_ENTRY_PREFILL || copies || entry == MLA_ENTRY_OUT_PROJECT)) w.wo = take(H * kDv * kD * 2);
     } else {
       // On-chip conversion: only the absorbed rows' GEMMs and decode read a
       // bf16 copy of W_kvb (and decode one of W_o).
       const int ng = (static_cast<int>(nq) + 3) / 4;
-      if (fp8 && ((attend && w.g_abs < ng) || dec)) w.wkvb = take(H * (kDn + kDv) * kL * 2);
-      if (fp8 && dec) w.wo = take(H * kDv * kD * 2);
+      if (fp8 && ((attend && w.g_abs < ng) || copies)) w.wkvb = take(H * (kDn + kDv) * kL * 2);
+      if (fp8 && copies) w.wo = take(H * kDv * kD * 2);
     }
   }
   w.total = off;
@@ -762,6 +779,76 @@ int launch_gemm_wo_m64(const DeviceState* ds, int M, int H, const void* attn, co
   cudaError_t le = cudaSuccess;
   rc = timed_launch(4, st, [&] {
     le = launch_kernel(mla::sum_segments_kernel, blocks, 256, 0, st, dependent, 1, part, M, N, K, bm, grid,
+                       static_cast<__nv_bfloat16*>(out), ds->err);
+  });
+  return le != cudaSuccess ? MLA_ERR_CUDA : rc;
+}
+
+template <class Cfg64, class Cfg128>
+int launch_m64_w8(const DeviceState* ds, const CUtensorMap& ta, const CUtensorMap& tw, int M, int N, int K,
+                  const mla::M64Batch& bt, int grid, const float* scale, float* part, void* out, int cls, cudaStream_t st,
+                  bool dependent) {
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+  cudaError_t le = cudaSuccess;
+  const int rc = timed_launch(cls, st, [&] {
+    if (M <= 64)
+      le = launch_kernel(mla::gemm_m64_w8_kernel<Cfg64>, grid, Cfg64::THREADS, Cfg64::SMEM_BYTES, st, dependent, 1, ta, tw,
+                         M, N, K, bt, scale, part, o, ds->err);
+    else
+      le = launch_kernel(mla::gemm_m64_w8_kernel<Cfg128>, grid, Cfg128::THREADS, Cfg128::SMEM_BYTES, st, dependent, 1, ta,
+                         tw, M, N, K, bt, scale, part, o, ds->err);
+  });
+  return le != cudaSuccess ? MLA_ERR_CUDA : rc;
+}
+
+// launch_gemm_absorb, launch_gemm_unabsorb and launch_gemm_wo_m64 of up to
+// kFewRows rows over e4m3 codes. o_lat comes with W_UV's scales multiplied in.
+int launch_w8_absorb(const DeviceState* ds, int H, int rows, const void* q_rows, const void* codes, const float* scale,
+                     void* qabs, cudaStream_t st) {
+  CUtensorMap ta, tw;
+  const uint64_t qw = static_cast<uint64_t>(H) * (kDn + kDr);
+  if (!map_2d(&ta, q_rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, qw, rows, qw * 2, 64, rows <= 64 ? 64 : 128) ||
+      !map_2d(&tw, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, kL, static_cast<uint64_t>(H) * (kDn + kDv), kL, 128, 64,
+              CU_TENSOR_MAP_SWIZZLE_NONE))
+    return MLA_ERR_CUDA;
+  const mla::M64Batch bt = {H, kDn + kDr, 0, kDn + kDv, kL, H * kL};
+  const int items = (rows <= 64 ? 1 : (rows + 127) / 128) * (kL / 128) * H;
+  return launch_m64_w8<GemmW8Abs64, GemmW8Abs128>(ds, ta, tw, rows, kL, kDn, bt, items < ds->sms ? items : ds->sms, scale,
+                                                  nullptr, qabs, 6, st, false);
+}
+
+int launch_w8_unabsorb(const DeviceState* ds, int H, int rows, const void* olat, const void* codes, void* attn_rows,
+                       cudaStream_t st) {
+  CUtensorMap ta, tw;
+  if (!map_2d(&ta, olat, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<uint64_t>(H) * kL, rows,
+              static_cast<uint64_t>(H) * kL * 2, 64, rows <= 64 ? 64 : 128) ||
+      !map_2d(&tw, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, kL, static_cast<uint64_t>(H) * (kDn + kDv), kL, 64, 128,
+              CU_TENSOR_MAP_SWIZZLE_NONE))
+    return MLA_ERR_CUDA;
+  const mla::M64Batch bt = {H, kL, kDn, kDn + kDv, kDv, H * kDv};
+  const int items = (rows <= 64 ? 1 : (rows + 127) / 128) * H;
+  return launch_m64_w8<GemmW8Unabs64, GemmW8Unabs128>(ds, ta, tw, rows, kDv, kL, bt, items < ds->sms ? items : ds->sms,
+                                                      nullptr, nullptr, attn_rows, 6, st, true);
+}
+
+int launch_w8_wo(const DeviceState* ds, int M, int H, const void* attn, const void* codes, const float* scale, float* part,
+                 void* out, cudaStream_t st) {
+  const int N = kD, K = H * kDv;
+  const int bm = M <= 64 ? 64 : 128;
+  CUtensorMap ta, tw;
+  if (!map_2d(&ta, attn, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, K, M, static_cast<uint64_t>(K) * 2, 64, bm) ||
+      !map_2d(&tw, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, N, K, N, 128, 64, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return MLA_ERR_CUDA;
+  const int64_t units = static_cast<int64_t>((M + bm - 1) / bm) * (N / 128) * (K / 64);
+  int grid = ds->sms < kStreamKCtas ? ds->sms : kStreamKCtas;
+  if (units < grid) grid = static_cast<int>(units);
+  const mla::M64Batch bt = {1, 0, 0, 0, 0, 0};
+  int rc = launch_m64_w8<GemmW8Wo64, GemmW8Wo128>(ds, ta, tw, M, N, K, bt, grid, scale, part, nullptr, 4, st, true);
+  if (rc != MLA_OK) return rc;
+  const int blocks = ((M + bm - 1) / bm) * (N / 128) * (bm / mla::kSumRows);
+  cudaError_t le = cudaSuccess;
+  rc = timed_launch(4, st, [&] {
+    le = launch_kernel(mla::sum_segments_kernel, blocks, 256, 0, st, true, 1, part, M, N, K, bm, grid,
                        static_cast<__nv_bfloat16*>(out), ds->err);
   });
   return le != cudaSuccess ? MLA_ERR_CUDA : rc;
@@ -1139,11 +1226,12 @@ mla::RopeTable rope_table(const mla_rope_table& t) {
 }
 
 // Attention of B trees of N nodes over the pages: q_abs (in the workspace) and
-// q's rotary part against the cache, into o_lat (in the workspace).
+// q's rotary part against the cache, into o_lat (in the workspace), times
+// W_UV's block scales if v_scale (W_kvb's scales) is given.
 int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pages& pg, const WsLayout& lay, void* ws,
                           const void* q, const void* kv, const void* pe, const int32_t* table,
                           const int32_t* cache_len, const int32_t* n_nodes, const int32_t* parents, float scale,
-                          cudaStream_t st, bool dependent) {
+                          const float* v_scale, cudaStream_t st, bool dependent) {
   mla::TreeParams p = {};
   p.B = d.B;
   p.N = d.T;
@@ -1157,6 +1245,7 @@ int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pa
   p.cache_len = cache_len;
   p.n_nodes = n_nodes;
   p.parents = parents;
+  p.v_scale = v_scale;
   p.olat = reinterpret_cast<__nv_bfloat16*>(ws_at(ws, lay.olat));
   p.ustart = reinterpret_cast<int64_t*>(ws_at(ws, lay.tree_start));
   p.part_o = reinterpret_cast<float*>(ws_at(ws, lay.tree_o));
@@ -1191,33 +1280,43 @@ int run_tree_decode(const DeviceState* ds, const mla_dims& d, const mla_pages& p
                     const int32_t* n_nodes, const int32_t* parents, const void* W_kvb, const float* W_kvb_scale,
                     const void* W_o, const float* W_o_scale, float scale, void* out, cudaStream_t st) {
   const int rows = d.B * d.T;
-  const void* wk = W_kvb;
-  int rc = MLA_OK;
-  if (d.wdtype == MLA_W_E4M3_BLOCK128) {
-    void* dq = ws_at(ws, lay.wkvb);
-    if ((rc = launch_dequant(ds, W_kvb, W_kvb_scale, dq, d.H * (kDn + kDv), kL, st)) != MLA_OK) return rc;
-    wk = dq;
-  }
+  const bool few = rows <= kFewRows, e4m3 = d.wdtype == MLA_W_E4M3_BLOCK128;
   void* qabs = ws_at(ws, lay.qabs);
   void* olat = ws_at(ws, lay.olat);
   void* attn = ws_at(ws, lay.attn);
-  // Few rows: after the first, each kernel is launched as a dependent of the one
-  // before, so that its set-up runs while that one ends. The pair GEMMs of more
-  // rows take plain launches.
-  const bool few = rows <= kFewRows;
+  int rc = MLA_OK;
+  if (few) {
+    // After the first, each kernel is launched as a dependent of the one before,
+    // so that its set-up runs while that one ends.
+    float* part = reinterpret_cast<float*>(ws_at(ws, lay.wo_part));
+    rc = e4m3 ? launch_w8_absorb(ds, d.H, rows, q, W_kvb, W_kvb_scale, qabs, st)
+              : launch_gemm_absorb(ds, d.H, rows, q, W_kvb, qabs, st);
+    if (rc != MLA_OK) return rc;
+    if ((rc = launch_tree_attention(ds, d, pg, lay, ws, q, kv, pe, table, cache_len, n_nodes, parents, scale,
+                                    e4m3 ? W_kvb_scale : nullptr, st, true)) != MLA_OK)
+      return rc;
+    rc = e4m3 ? launch_w8_unabsorb(ds, d.H, rows, olat, W_kvb, attn, st)
+              : launch_gemm_unabsorb(ds, d.H, rows, olat, W_kvb, attn, st, true);
+    if (rc != MLA_OK) return rc;
+    return e4m3 ? launch_w8_wo(ds, rows, d.H, attn, W_o, W_o_scale, part, out, st)
+                : launch_gemm_wo_m64(ds, rows, d.H, attn, W_o, part, out, st, true);
+  }
+  // More rows: the pair GEMMs, over bf16 copies of e4m3 weights.
+  const void* wk = W_kvb;
   const void* wo = W_o;
-  if (d.wdtype == MLA_W_E4M3_BLOCK128) {
-    void* dq = ws_at(ws, lay.wo);
-    if ((rc = launch_dequant(ds, W_o, W_o_scale, dq, d.H * kDv, kD, st)) != MLA_OK) return rc;
-    wo = dq;
+  if (e4m3) {
+    void* dk = ws_at(ws, lay.wkvb);
+    void* dw = ws_at(ws, lay.wo);
+    if ((rc = launch_dequant(ds, W_kvb, W_kvb_scale, dk, d.H * (kDn + kDv), kL, st)) != MLA_OK) return rc;
+    if ((rc = launch_dequant(ds, W_o, W_o_scale, dw, d.H * kDv, kD, st)) != MLA_OK) return rc;
+    wk = dk;
+    wo = dw;
   }
   if ((rc = launch_gemm_absorb(ds, d.H, rows, q, wk, qabs, st)) != MLA_OK) return rc;
-  if ((rc = launch_tree_attention(ds, d, pg, lay, ws, q, kv, pe, table, cache_len, n_nodes, parents, scale, st, few)) !=
-      MLA_OK)
+  if ((rc = launch_tree_attention(ds, d, pg, lay, ws, q, kv, pe, table, cache_len, n_nodes, parents, scale, nullptr, st,
+                                  false)) != MLA_OK)
     return rc;
-  if ((rc = launch_gemm_unabsorb(ds, d.H, rows, olat, wk, attn, st, few)) != MLA_OK) return rc;
-  if (lay.wo_part != kNone)
-    return launch_gemm_wo_m64(ds, rows, d.H, attn, wo, reinterpret_cast<float*>(ws_at(ws, lay.wo_part)), out, st, few);
+  if ((rc = launch_gemm_unabsorb(ds, d.H, rows, olat, wk, attn, st)) != MLA_OK) return rc;
   return launch_gemm_wo(ds, rows, d.H, attn, wo, out, st);
 }
 
