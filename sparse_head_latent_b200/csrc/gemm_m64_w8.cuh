@@ -12,10 +12,12 @@
 //           attention has multiplied into o_lat before rounding it
 //   W_o     (stream-K): bf16(code * scale), rounded once, as the copy would be
 //
-// Roles (448 threads, one CTA per SM): warp 0 TMA producer; warp 1 tensor memory
-// and UMMA issuer; warps 2..5 epilogue; warps 6..13 converters. A stage holds A
-// [BM x 64] and the codes of [64 x 128] weights (8 KB); three 16 KB buffers hold
-// converted operands. Work (segments, stream-K shares, batches) as in
+// Roles (480 threads, one CTA per SM): warp 0 asks for codes, warp 14 for A; warp
+// 1 tensor memory and UMMA issuer; warps 2..5 epilogue; warps 6..13 converters,
+// two teams that take tiles in turn. Codes ([64 x 128], 8 KB), A ([BM x 64]) and
+// converted operands (16 KB) have rings of their own: with a common stage, five
+// to seven of which fit, only 40 to 56 KB of codes were in flight per SM, and W_o's
+// 117 MB took 53 us. Work (segments, stream-K shares, batches) as in
 // gemm_m64.cuh.
 #pragma once
 
@@ -31,14 +33,14 @@ template <int BM_, bool B_MN_MAJOR_, bool BATCH_>
 struct GemmM64W8Cfg {
   static constexpr int BM = BM_, BN = 128, BK = 64;
   static constexpr bool B_MN_MAJOR = B_MN_MAJOR_, BATCH = BATCH_;
-  static constexpr int STAGES = BM_ == 64 ? 10 : 7;
-  static constexpr int A_BYTES = BM * BK * 2, W_BYTES = BK * BN;
-  static constexpr int STAGE_BYTES = A_BYTES + W_BYTES;
-  static constexpr int BUFS = 3, BUF_BYTES = BK * BN * 2;
-  static constexpr int CONVERTERS = 8;
-  static constexpr int THREADS = 192 + 32 * CONVERTERS;
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * BUFS + 4;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + BUFS * BUF_BYTES + NUM_BARS * 8 + 16;
+  static constexpr int A_STAGES = BM_ == 64 ? 6 : 5, W_STAGES = BM_ == 64 ? 14 : 10, BUFS = 4;
+  static constexpr int A_BYTES = BM * BK * 2, W_BYTES = BK * BN, BUF_BYTES = BK * BN * 2;
+  static constexpr int CONVERTERS = 16, TEAMS = 4, TEAM = CONVERTERS / TEAMS;
+  static constexpr int THREADS = 192 + 32 * CONVERTERS + 32;
+  static constexpr int NUM_BARS = 2 * (A_STAGES + W_STAGES + BUFS) + 4;
+  static constexpr int A0 = 0, BUF0 = A0 + A_STAGES * A_BYTES, W0 = BUF0 + BUFS * BUF_BYTES;
+  static constexpr int BARS = W0 + W_STAGES * W_BYTES;
+  static constexpr int SMEM_BYTES = 1024 + BARS + NUM_BARS * 8 + 16;
   static constexpr uint32_t TMEM_COLS = 256;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -49,7 +51,7 @@ template <bool SCALED>
 __device__ __forceinline__ uint32_t e4m3x2_bf16x2(uint32_t codes, float s) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xffffu), __NV_E4M3);
   float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  if (SCALED) f.x *= s, f.y *= s;
+  if (SCALED) fma2_scalar(f.x, f.y, s, -0.f);  // one packed product; + -0 changes nothing
   return pack_bf16x2(f.x, f.y);
 }
 
@@ -61,26 +63,30 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, int M, int N, int K,
                    const M64Batch bt, const float* __restrict__ scale, float* __restrict__ part,
                    __nv_bfloat16* __restrict__ out, int* err) {
-  constexpr int BK = Cfg::BK, S = Cfg::STAGES, NB = Cfg::BUFS;
+  constexpr int BK = Cfg::BK, SA = Cfg::A_STAGES, SW = Cfg::W_STAGES, NB = Cfg::BUFS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* bufs = smem + S * Cfg::STAGE_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(bufs + NB * Cfg::BUF_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::BARS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
   int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S;
-  const uint32_t bfull0 = empty0 + 8 * S, bempty0 = bfull0 + 8 * NB;
+  const uint32_t afull0 = smem_u32(bars), aempty0 = afull0 + 8 * SA;
+  const uint32_t wfull0 = aempty0 + 8 * SA, wempty0 = wfull0 + 8 * SW;
+  const uint32_t bfull0 = wempty0 + 8 * SW, bempty0 = bfull0 + 8 * NB;
   const uint32_t accf0 = bempty0 + 8 * NB, acce0 = accf0 + 16;
   const int warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, 1);
+    for (int s = 0; s < SA; ++s) {
+      mbar_init(afull0 + 8 * s, 1);
+      mbar_init(aempty0 + 8 * s, 1);
+    }
+    for (int s = 0; s < SW; ++s) {
+      mbar_init(wfull0 + 8 * s, 1);
+      mbar_init(wempty0 + 8 * s, Cfg::TEAM);
     }
     for (int b = 0; b < NB; ++b) {
-      mbar_init(bfull0 + 8 * b, Cfg::CONVERTERS);
+      mbar_init(bfull0 + 8 * b, Cfg::TEAM);
       mbar_init(bempty0 + 8 * b, 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -108,112 +114,103 @@ gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   M64Work work(M, N, K, bt.count, Cfg::BM, Cfg::BATCH);
   M64Seg sg;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == Cfg::THREADS / 32 - 1) {
     if (lane == 0) {
-      // ---------------- TMA producer. The weights do not come from the kernel
-      // before this one: the first stages' codes are asked for at once, A after it.
-      int it = 0, asked = 0;
+      // ---------------- TMA producers. The weights do not come from the kernels
+      // of this chain: their codes are asked for at once, A after the kernel before.
+      const bool codes = warp == 0;
+      if (!codes) griddep_wait();
+      const uint32_t full0 = codes ? wfull0 : afull0, empty0 = codes ? wempty0 : aempty0;
+      const uint32_t base = smem_u32(smem) + (codes ? Cfg::W0 : Cfg::A0), bytes = codes ? Cfg::W_BYTES : Cfg::A_BYTES;
+      const int stages = codes ? SW : SA;
+      int s = 0;
+      uint32_t parity = 1;
       bool ok = true;
-      {
-        M64Work ahead = work;
-        M64Seg a;
-        while (asked < S && ahead.next(a)) {
-          for (int kb = a.kb0; kb < a.kb1 && asked < S; ++kb, ++asked) {
-            mbar_arrive_expect_tx(full0 + 8 * asked, Cfg::STAGE_BYTES);
-            const uint32_t w = smem_u32(smem + asked * Cfg::STAGE_BYTES) + Cfg::A_BYTES;
-            const int r = bt.b_row0 + a.z * bt.b_step;
-            if constexpr (Cfg::B_MN_MAJOR)
-              tma_load_2d(w, &tmW, full0 + 8 * asked, a.nt * Cfg::BN, r + kb * BK);
-            else
-              tma_load_2d(w, &tmW, full0 + 8 * asked, kb * BK, r + a.nt * Cfg::BN);
-          }
-        }
-      }
-      griddep_wait();
       while (ok && work.next(sg)) {
-        for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-          const int s = it % S;
-          const uint32_t fb = full0 + 8 * s;
-          const uint32_t sa = smem_u32(smem + s * Cfg::STAGE_BYTES);
-          const int k = kb * BK;
-          if (it >= asked) {
-            if (!mbar_wait(empty0 + 8 * s, ((it / S) & 1) ^ 1, ab, kErrWaitConsumer)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(fb, Cfg::STAGE_BYTES);
-            const int r = bt.b_row0 + sg.z * bt.b_step;
-            if constexpr (Cfg::B_MN_MAJOR)
-              tma_load_2d(sa + Cfg::A_BYTES, &tmW, fb, sg.nt * Cfg::BN, r + k);
-            else
-              tma_load_2d(sa + Cfg::A_BYTES, &tmW, fb, k, r + sg.nt * Cfg::BN);
+        const int wrow = bt.b_row0 + sg.z * bt.b_step;
+        for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
+          if (!mbar_wait_short(empty0 + 8 * s, parity, ab, kErrWaitConsumer)) {
+            ok = false;
+            break;
           }
-          tma_load_2d(sa, &tmA, fb, sg.z * bt.a_step + k, sg.mt * Cfg::BM);  // rows past M read as zero
+          const uint32_t fb = full0 + 8 * s, dst = base + s * bytes;
+          const int k = kb * BK;
+          mbar_arrive_expect_tx(fb, bytes);
+          if (!codes)
+            tma_load_2d(dst, &tmA, fb, sg.z * bt.a_step + k, sg.mt * Cfg::BM);  // rows past M read as zero
+          else if constexpr (Cfg::B_MN_MAJOR)
+            tma_load_2d(dst, &tmW, fb, sg.nt * Cfg::BN, wrow + k);
+          else
+            tma_load_2d(dst, &tmW, fb, k, wrow + sg.nt * Cfg::BN);
+          if (++s == stages) s = 0, parity ^= 1;
         }
       }
       if (!ok) spin_ns(2000000);  // let issued loads land before the CTA can exit
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- UMMA issuer
-      constexpr uint32_t idesc = idesc_bf16_f32(Cfg::BM, Cfg::BN, 0, Cfg::B_MN_MAJOR ? 1 : 0);
-      int it = 0, t = 0;
-      bool ok = true;
-      for (; ok && work.next(sg); ++t) {
-        const int a = t & 1;
-        if (!mbar_wait(acce0 + 8 * a, ((t >> 1) & 1) ^ 1, ab, kErrWaitEpilogue)) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + a * Cfg::BN;
-        for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-          const int s = it % S, b = it % NB;
-          if (!mbar_wait(full0 + 8 * s, (it / S) & 1, ab, kErrWaitTma) ||
-              !mbar_wait(bfull0 + 8 * b, (it / NB) & 1, ab, kErrWaitSoftmax)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * Cfg::STAGE_BYTES), sb = smem_u32(bufs + b * Cfg::BUF_BYTES);
-#pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_ss(d, smem_desc_sw128(sa + k * 32, 16, 1024),
-                    Cfg::B_MN_MAJOR ? smem_desc_sw128(sb + k * 16 * 128, BK * 128, 1024)
-                                    : smem_desc_sw128(sb + k * 32, 16, 1024),
-                    idesc, (kb != sg.kb0 || k != 0) ? 1u : 0u);
-          umma_commit(empty0 + 8 * s);
-          umma_commit(bempty0 + 8 * b);
+    // ---------------- UMMA issuer, the whole warp (see umma_ss_pair_x4)
+    constexpr uint32_t idesc = idesc_bf16_f32(Cfg::BM, Cfg::BN, 0, Cfg::B_MN_MAJOR ? 1 : 0);
+    const uint32_t issue = elect_lane();
+    const uint64_t da = smem_desc_sw128(smem_u32(smem + Cfg::A0), 16, 1024);
+    const uint64_t db = smem_desc_sw128(smem_u32(smem + Cfg::BUF0), Cfg::B_MN_MAJOR ? BK * 128 : 16, 1024);
+    uint32_t s = 0, sp = 0, b = 0, bp = 0;
+    int t = 0, last = -1;
+    bool ok = true;
+    for (; ok && work.next(sg); ++t) {
+      const int a = t & 1;
+      if (!mbar_wait_short(acce0 + 8 * a, ((t >> 1) & 1) ^ 1, ab, kErrWaitEpilogue)) break;
+      tc_fence_after();
+      const uint32_t d = tmem_base + a * Cfg::BN;
+#pragma unroll 1
+      for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
+        if (!mbar_wait_short(afull0 + 8 * s, sp, ab, kErrWaitTma) || !mbar_wait_short(bfull0 + 8 * b, bp, ab, kErrWaitSoftmax)) {
+          ok = false;
+          break;
         }
-        if (!ok) break;
-        umma_commit(accf0 + 8 * a);
+        tc_fence_after();
+        umma_ss_x4<2, Cfg::B_MN_MAJOR ? 128 : 2>(d, da + s * (Cfg::A_BYTES >> 4), db + b * (Cfg::BUF_BYTES >> 4), idesc,
+                                                 kb != sg.kb0 ? 1u : 0u, issue);
+        umma_commit_warp(aempty0 + 8 * s, issue);
+        umma_commit_warp(bempty0 + 8 * b, issue);
+        last = static_cast<int>(2 * s + sp);
+        if (++s == SA) s = 0, sp ^= 1;
+        if (++b == NB) b = 0, bp ^= 1;
       }
-      if (!ok && it > 0) {
-        const int i = it - 1;
-        mbar_wait_drain(empty0 + 8 * (i % S), (i / S) & 1);
-      }
+      if (!ok) break;
+      umma_commit_warp(accf0 + 8 * a, issue);
     }
+    if (!ok && last >= 0) mbar_wait_drain(aempty0 + 8 * (last >> 1), last & 1);
   } else if (warp >= 6) {
     // ---------------- converters: 16 codes at a time, 512 such pieces per stage.
     // A row of 64 codes (64 bytes, four pieces) becomes a 128-byte operand row:
     // stored [K, N], code row k holds two, of the 64-column chunks 0 and 1;
     // stored [N, K], one. Lanes take neighbouring pieces: loads and both
     // stores are free of bank conflicts.
-    const int me = static_cast<int>(threadIdx.x) - 192;
+    constexpr int PIECES = 512 / (32 * Cfg::TEAM);
+    const int me = (static_cast<int>(threadIdx.x) - 192) % (32 * Cfg::TEAM), team = (warp - 6) / Cfg::TEAM;
     int it = 0;
     bool ok = true;
     while (ok && work.next(sg)) {
+#pragma unroll 1
       for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-        const int s = it % S, b = it % NB;
+        if (it % Cfg::TEAMS != team) continue;
+        const int s = it % SW, b = it % NB;
         float f = 1.f;
         if constexpr (!Cfg::BATCH) f = __ldg(scale + static_cast<int64_t>(kb >> 1) * (N / 128) + sg.nt);
-        if (!(ok = warp_wait_all(bempty0 + 8 * b, ((it / NB) & 1) ^ 1, ab, kErrWaitMma) &&
-                   warp_wait_all(full0 + 8 * s, (it / S) & 1, ab, kErrWaitTma)))
-          break;
-        const uint8_t* src = smem + s * Cfg::STAGE_BYTES + Cfg::A_BYTES;
-        uint8_t* dst = bufs + b * Cfg::BUF_BYTES;
+        if (!(ok = warp_wait_all(wfull0 + 8 * s, (it / SW) & 1, ab, kErrWaitTma))) break;
+        const uint8_t* src = smem + Cfg::W0 + s * Cfg::W_BYTES;
+        uint4 w[PIECES];
 #pragma unroll
-        for (int i = 0; i < 512 / (32 * Cfg::CONVERTERS); ++i) {
-          const int piece = me + i * 32 * Cfg::CONVERTERS, row64 = piece >> 2, q = piece & 3;
-          const uint4 w = *reinterpret_cast<const uint4*>(src + piece * 16);
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+        for (int i = 0; i < PIECES; ++i)
+          w[i] = *reinterpret_cast<const uint4*>(src + (me + i * 32 * Cfg::TEAM) * 16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(wempty0 + 8 * s);
+        if (!(ok = warp_wait_all(bempty0 + 8 * b, ((it / NB) & 1) ^ 1, ab, kErrWaitMma))) break;
+        uint8_t* dst = smem + Cfg::BUF0 + b * Cfg::BUF_BYTES;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+          const int piece = me + i * 32 * Cfg::TEAM, row64 = piece >> 2, q = piece & 3;
+          const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
           uint32_t o[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {

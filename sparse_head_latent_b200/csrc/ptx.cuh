@@ -530,6 +530,36 @@ __device__ __forceinline__ void umma_ss_pair_x4(uint32_t d_tmem, uint64_t a_desc
       : "memory");
 }
 
+// umma_ss_pair_x4 for one CTA.
+template <int DA, int DB>
+__device__ __forceinline__ void umma_ss_x4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate_first, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, t;\n\t"
+      ".reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 a1, %1, %6;\n\tadd.s64 b1, %2, %9;\n\t"
+      "add.s64 a2, %1, %7;\n\tadd.s64 b2, %2, %10;\n\t"
+      "add.s64 a3, %1, %8;\n\tadd.s64 b3, %2, %11;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate_first), "r"(issue), "n"(DA), "n"(2 * DA), "n"(3 * DA),
+      "n"(DB), "n"(2 * DB), "n"(3 * DB)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_warp(uint32_t bar, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(issue)
+      : "memory");
+}
+
 // umma_ss_pair_x4 with A in tensor memory (K = 16: 8 columns).
 template <int DB>
 __device__ __forceinline__ void umma_ts_pair_x4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
