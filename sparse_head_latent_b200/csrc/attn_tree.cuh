@@ -90,34 +90,38 @@ __device__ __forceinline__ void tree_extent(const TreeParams& p, int len, int no
   blocks = nodes > 0 ? (len + nodes + kTreeBlock - 1) / kTreeBlock : 0;
 }
 
-// A pair's next run of blocks [j0, j1) of one tile.
-struct TreeSeg {
-  int b, tile, j0, j1, len, nodes, blocks;
-  bool first;  // the pair's first run
+// A run of a pair's work: blocks [j0, j1) of one tile.
+struct TreeRun {
+  int b, tile, j0, j1;
+  int len, nodes, blocks;  // of sequence b
+  int flags;               // 1: the pair's first run, 2: another one follows
 };
 
-// Walks a pair's share [u, u1) of the units; every role walks it alike.
+// Where a pair stands in its share of the units.
 struct TreeWork {
-  int64_t u0, u, u1, base;  // base: first unit of sequence b
-  int b;
-  __device__ __noinline__ bool next(const TreeParams& p, TreeSeg& s) {
-    if (u >= u1) return false;
-    int tiles;
-    while (true) {
-      tree_lengths(p, b, s.len, s.nodes);
-      tree_extent(p, s.len, s.nodes, tiles, s.blocks);
-      const int64_t units = static_cast<int64_t>(tiles) * s.blocks;
-      if (u < base + units) break;
-      base += units;
-      ++b;
+  int64_t left;                   // units still to walk
+  int b, tile, j;                 // where the next run begins
+  int len, nodes, tiles, blocks;  // of sequence b
+  int first;
+  __device__ __forceinline__ TreeRun next(const TreeParams& p) {
+    while (tile >= tiles) {
+      tree_lengths(p, ++b, len, nodes);
+      tree_extent(p, len, nodes, tiles, blocks);
+      tile = 0;
     }
-    s.b = b;
-    s.tile = static_cast<int>((u - base) / s.blocks);
-    s.j0 = static_cast<int>((u - base) % s.blocks);
-    s.j1 = static_cast<int>(min(static_cast<int64_t>(s.blocks), s.j0 + (u1 - u)));
-    s.first = u == u0;
-    u += s.j1 - s.j0;
-    return true;
+    TreeRun r;
+    r.b = b;
+    r.tile = tile++;
+    r.j0 = j;
+    r.j1 = left < blocks - j ? j + static_cast<int>(left) : blocks;
+    r.len = len;
+    r.nodes = nodes;
+    r.blocks = blocks;
+    left -= r.j1 - j;
+    r.flags = first | (left > 0 ? 2 : 0);
+    first = 0;
+    j = 0;
+    return r;
   }
 };
 
@@ -139,7 +143,9 @@ struct TreeSmem {
   static constexpr int P = Q + Q_CHUNKS * CHUNK;   // two [64 rows x 64 keys] chunks
   static constexpr int XCHG = P + 2 * CHUNK;       // [2][4][64] floats
   static constexpr int BARS = XCHG + 2 * 4 * 64 * 4;
-  static constexpr int BYTES = BARS + 512;
+  static constexpr int START = BARS + 400;         // where the share begins: sequence, tile, block
+  static constexpr int RUNS = BARS + 416;          // four TreeRuns, published by the producer of keys
+  static constexpr int BYTES = RUNS + 4 * 32;
 };
 static_assert(TreeSmem::BYTES <= 232448, "shared memory per CTA");
 
@@ -155,23 +161,22 @@ enum : int {
   kTreePVDone,                                  // P.V of a block is done
   kTreeRopeFull,                                // (L) per rope slot: the chunk landed in both CTAs
   kTreeQFull = kTreeRopeFull + TreeSmem::ROPES,                                   // (L) Q's shared-memory part landed in both CTAs
-  kTreeQGroups,                                 // the three groups of its tensor-memory part landed in this CTA; two,
+  kTreeRun,                                     // a run's description is in the ring; two, taken in turn
+  kTreeQGroups = kTreeRun + 2,                  // the three groups of its tensor-memory part landed in this CTA; two,
                                                 // taken in turn, since a run of one block is requested two runs ahead
   kTreeQReady = kTreeQGroups + 2,                                // (L) they are in tensor memory (sixteen warps)
   kTreePFull,                                   // (L) P of both CTAs is written (sixteen warps)
   kTreeTail,                                    // the reloaded values of a block with drafted keys landed in this
                                                 // CTA; two, taken in turn
-  kTreeDrain = kTreeTail + 2,
+  kTreeXchg = kTreeTail + 2,                    // per 32 rows: their four softmax warps have written their values
+  kTreeOut = kTreeXchg + 2,                     // the eight softmax warps of this CTA meet
+  kTreeDrain,
   kTreeBars
 };
-static_assert(8 * kTreeBars + 8 <= 384, "barriers, then the share's start at byte 384");
+static_assert(8 * kTreeBars + 8 <= 400 && sizeof(TreeRun) == 32, "layout behind the barriers");
 
 constexpr uint32_t kTreeColS = 256;  // S; O at 0 and 128
 constexpr uint32_t kTreeColQ = 320;  // Q's first six chunks, 32 columns each
-
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 
 // Nodes that node j of sequence b sees, as bits (itself included); every lane
 // of the warp asks for its own j. The parents of nodes `lane` and `lane + 32`
@@ -234,7 +239,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BARS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kTreeBars);
   int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
-  int64_t* start = reinterpret_cast<int64_t*>(smem + S::BARS + 384);  // units, first unit of the share's sequence, it
+  int* start = reinterpret_cast<int*>(smem + S::START);
+  TreeRun* run_ring = reinterpret_cast<TreeRun*>(smem + S::RUNS);
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
   const int warp = threadIdx.x >> 5;
@@ -243,7 +249,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kTreeBars; ++i) mbar_init(bar(i), i == kTreeSFree || i == kTreePFull || i == kTreeQReady ? 16 : 1);
+    for (int i = 0; i < kTreeBars; ++i) {
+      const bool both = i == kTreeSFree || i == kTreePFull || i == kTreeQReady;
+      mbar_init(bar(i), both ? 16 : i == kTreeOut ? 8 : i == kTreeXchg || i == kTreeXchg + 1 ? 4 : 1);
+    }
     *abort_word = 0;
     fence_barrier_init();
   }
@@ -295,32 +304,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         const int64_t units = static_cast<int64_t>(tiles) * blocks;
         if (mark) p.ustart[b] = at;
         if (u0 >= at && u0 < at + units) {
-          start[0] = at;
-          start[1] = b;
+          start[0] = b;
+          start[1] = static_cast<int>((u0 - at) / blocks);
+          start[2] = static_cast<int>((u0 - at) % blocks);
         }
         at += units;
       }
     }
     if (mark && threadIdx.x == 0) p.ustart[p.B] = total;
-    work.u0 = work.u = u0;
-    work.u1 = tree_share(total, pair + 1, pairs);
+    work.left = tree_share(total, pair + 1, pairs) - u0;
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrival
   tc_fence_after();
   griddep_launch();
-  work.base = start[0];
-  work.b = static_cast<int>(start[1]);
+  const bool busy = work.left > 0;  // the pair has work at all
   const uint32_t tmem = *tmem_slot;
   const Abort ab{abort_word, p.err};
-  // The pair's next run, in registers (next() itself stays out of line).
-  auto next_run = [&](TreeSeg& run) -> bool {
-    TreeSeg t;
-    const bool more = work.next(p, t);
-    run = t;
-    return more;
-  };
 
   if (warp == 0 || warp == kTreeThreads / 32 - 1) {
     // ---------------- producers: whole warps on one path, one lane issues
@@ -343,7 +344,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
     auto place = [&](int j) -> int64_t {
       return static_cast<int64_t>(j) * kTreeBlock + 64 * half + (static_cast<int64_t>(lane) << p.box_shift);
     };
-    TreeSeg sg = {};
+    TreeRun sg = {};
     auto entry_of = [&](int j) -> int {
       int e = 0;
       if (lane < boxes && j < sg.j1 && place(j) < sg.len + sg.nodes)
@@ -379,7 +380,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       const uint32_t rope0 = smem_u32(smem + S::ROPE), empty0 = bar(kTreeEmpty), rfull0 = bar(kTreeRopeFull);
       const uint32_t kfull0_leader = mapa_shared(kfull0, 0), rfull0_leader = mapa_shared(rfull0, 0);
       uint32_t ks = 0, parity = 0;  // the next group to fill
-      while (ok && next_run(sg)) {
+      if (busy) {
+        work.b = start[0];
+        work.tile = start[1];
+        work.j = start[2];
+        work.first = 1;
+        tree_lengths(p, work.b, work.len, work.nodes);
+        tree_extent(p, work.len, work.nodes, work.tiles, work.blocks);
+      }
+      while (ok && work.left > 0) {
+        // This warp alone walks the share; the others take the run from here. The
+        // slot is free: what the ring of groups does not hold any more is through,
+        // and with seven groups a run or more, it holds parts of two.
+        sg = work.next(p);
+        if (lane == 0) {
+          run_ring[runs & 3] = sg;
+          mbar_arrive(bar(kTreeRun + (runs & 1)));
+        }
+        __syncwarp();
         int entry = entry_of(sg.j0);
         const int qrow = sg.b * p.N * p.H + sg.tile * kTreeRows + 64 * rank;
         const uint32_t landed = bar(kTreeQGroups + (runs++ & 1));
@@ -418,7 +436,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       const uint32_t q0 = smem_u32(smem + S::Q);
       uint32_t vs = 0;  // the next group to fill again
       int tails = 0;    // blocks with drafted keys so far
-      while (ok && next_run(sg)) {
+      bool more = busy;
+      while (ok && more) {
+        if (!(ok = warp_wait_all(bar(kTreeRun + (runs & 1)), (runs >> 1) & 1, ab, kErrWaitConsumer))) break;
+        sg = run_ring[runs++ & 3];
+        more = sg.flags & 2;
         int entry = entry_of(sg.j0);
         // Q's shared-memory part: Q.K^T of the run before is done. Rows past the
         // sequence's last belong to another sequence or to none, and are not stored.
@@ -514,11 +536,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         ++commits;
         return true;
       };
-      TreeSeg sg = {};
-      while (ok && next_run(sg)) {
-        const int n = sg.j1 - sg.j0;
+      bool more = busy;
+      while (ok && more) {
         if (!(ok = mbar_wait_short(bar(kTreeQFull), seg & 1, ab, kErrWaitTma))) break;
         if (!(ok = mbar_wait_short(bar(kTreeQReady), seg & 1, ab, kErrWaitSoftmax))) break;
+        const int n = run_ring[seg & 3].j1 - run_ring[seg & 3].j0;
+        more = run_ring[seg & 3].flags & 2;
         for (int i = 0; i < S::Q_GROUPS; ++i) {  // Q's groups are free: nothing else has read them
           umma_commit_pair_warp(empty0 + 8 * ks, 0x3, issue);
           if (++ks == S::GROUPS) ks = 0, kparity ^= 1;
@@ -541,9 +564,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
   } else {
     // ---------------- softmax. Quadrant of tensor-memory lanes q, half ch of
     // its 64 key columns: row (32 q + lane) mod 64, keys 64 (q / 2) + 32 ch ..
-    // + 32 of the block. The four warps of 32 rows meet at a named barrier for
-    // every block, also after a wait has failed (`ok` false: no more waits, no
-    // more work), so that none is left at it.
+    // + 32 of the block.
     const int quad = warp & 3, ch = (warp - 2) >> 2;
     const int row = (32 * quad + lane) & 63, lh = quad >> 1, part = 2 * lh + ch;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -552,15 +573,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
     const float c = p.scale_log2;
     const uint32_t p_full = mapa_shared(bar(kTreePFull), 0), s_free = mapa_shared(bar(kTreeSFree), 0);
     bool ok = true;
-    int g = 0, tails = 0, turn = 0, runs = 0;  // runs: whose Q has been loaded
+    int g = 0, tails = 0, turn = 0, meets = 0, runs = 0;  // runs: whose Q has been loaded
     // The four threads' values of this row.
-    auto exchange = [&](float v, float (&all)[4]) {
+    auto exchange = [&](float v, float (&all)[4]) -> bool {
       float* x = xchg + (turn & 1) * 256;
-      ++turn;
       x[part * 64 + row] = v;
-      named_barrier(1 + (quad & 1), 128);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kTreeXchg + (quad & 1)));
+      if (!warp_wait_all(bar(kTreeXchg + (quad & 1)), turn & 1, ab, kErrWaitSoftmax)) return false;
+      ++turn;
 #pragma unroll
       for (int i = 0; i < 4; ++i) all[i] = x[i * 64 + row];
+      return true;
+    };
+    // The eight warps meet.
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kTreeOut));
+      return warp_wait_all(bar(kTreeOut), meets++ & 1, ab, kErrWaitSoftmax);
     };
     // Q's groups (positions `at` and on of the ring) into tensor memory: with M =
     // 128 both lane r and lane r + 64 hold row r; this warp's three chunks of
@@ -568,7 +598,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
     auto load_q = [&](int at) -> bool {
       if (!warp_wait_all(bar(kTreeQGroups + (runs & 1)), (runs >> 1) & 1, ab, kErrWaitTma)) return false;
       ++runs;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < 3; ++i) {
         const int c = 3 * ch + i;
         const uint8_t* src = smem + S::RING + (at + (c >> 1)) % S::GROUPS * S::GROUP + (c & 1) * S::CHUNK + row * 128;
@@ -586,24 +616,26 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       if (lane == 0) mbar_arrive_remote(mapa_shared(bar(kTreeQReady), 0));
       return true;
     };
-    TreeSeg sg = {};
-    bool more = next_run(sg);
-    if (more) ok = load_q(0);
-    while (more) {
+    if (busy) ok = load_q(0);
+    bool more = busy;
+    while (ok && more) {
+      const TreeRun sg = run_ring[(runs - 1) & 3];
+      more = sg.flags & 2;
       const int r = sg.tile * kTreeRows + 64 * rank + row;  // row of the sequence: node * H + head
       const int live = sg.nodes * p.H;
       const bool has_tail = static_cast<int64_t>(sg.j1) * kTreeBlock > sg.len;
       const uint64_t sees = has_tail ? tree_ancestors(p, sg.b, min(r / p.H, kTreeMax)) : 0ull;
       const int total = sg.len + sg.nodes;
       float m_run = -INFINITY, l_run = 0.f;
+#pragma unroll 1
       for (int j = sg.j0; j < sg.j1; ++j, ++g) {
-        if (ok) ok = warp_wait_all(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma);
+        if (!(ok = warp_wait_all(bar(kTreeSFull + (g & 1)), (g >> 1) & 1, ab, kErrWaitMma))) break;
         tc_fence_after();
         float x[32];
         tmem_ld32(tl + kTreeColS + 32u * ch, *reinterpret_cast<uint32_t(*)[32]>(x));
         tc_fence_before();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive_remote(s_free);
+        if (lane == 0) mbar_arrive_remote(s_free);
         const int64_t t0 = static_cast<int64_t>(j) * kTreeBlock;
         const bool tail = t0 + kTreeBlock > sg.len;
         if (tail) {
@@ -622,7 +654,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], x[28 + i]);
         float all[4];
-        exchange(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), all);
+        if (!(ok = exchange(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), all))) break;
         // Lazy rescaling: the running maximum moves only when a block exceeds
         // it by more than 8 (in log2), so P < 2^8 and O is rarely touched.
         const float m_new = fmaxf(m_run, fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3])) * c);
@@ -645,8 +677,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         }
         l_run = l_run * alpha + ((sm[0] + sm[1]) + (sm[2] + sm[3]));
         // P.V of the block before must be done before P is overwritten and O rescaled.
-        if (g > 0 && ok) ok = warp_wait_all(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma);
-        if (ok && j > sg.j0 && __any_sync(0xffffffffu, resc)) {
+        if (g > 0 && !(ok = warp_wait_all(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma))) break;
+        if (j > sg.j0 && __any_sync(0xffffffffu, resc)) {
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < 128; c0 += 32) {
@@ -657,20 +689,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
             tmem_st32(tl + 128u * ch + c0, o);
           }
         }
-        if (ok) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(prow + (((4 * ch + i) ^ (row & 7)) << 4)) =
-                make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-        }
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(prow + (((4 * ch + i) ^ (row & 7)) << 4)) =
+              make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
         if (tail) {
           // The values from the first drafted key on: those behind the last
           // position hold whatever the page held before, and 0 * NaN is
           // NaN, so they are zeroed; so is what is not finite in a drafted
           // key's values (a row that sees it gets its NaN from the score).
-          if (ok) ok = warp_wait_all(bar(kTreeTail + (tails & 1)), (tails >> 1) & 1, ab, kErrWaitTma);
+          if (!(ok = warp_wait_all(bar(kTreeTail + (tails & 1)), (tails >> 1) & 1, ab, kErrWaitTma))) break;
           ++tails;
-          if (ok) {
+          {
             const int who = static_cast<int>(threadIdx.x) - 64;  // 256 threads: piece who % 32 of key who / 32
             const int piece = who & 31, h = piece >> 4, chunk = (piece >> 3) & 1;
             for (int k = static_cast<int>(max(int64_t(0), sg.len - t0)) + (who >> 5); k < kTreeBlock; k += 8) {
@@ -698,42 +728,51 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         // tensor core reads it: each lane's fence has put its stores before that
         // before lane 0 arrives. A cluster-scope release here, which orders them
         // for the other SM's threads too, took 1300 to 2100 clk a block.
-        if (ok && lane == 0) mbar_arrive_remote(p_full);
+        if (lane == 0) mbar_arrive_remote(p_full);
       }
+      if (!ok) break;
       // ---------------- the run's result: o_lat, or its part of it. The next
       // run's Q first: its products have no more use for this one's.
-      TreeSeg nx = {};
-      more = next_run(nx);
-      if (more && ok) ok = load_q(4 * g + S::Q_GROUPS * runs);
+      if (more && !(ok = load_q(4 * g + S::Q_GROUPS * runs))) break;
       float all[4];
-      exchange(l_run, all);
-      if (ok) ok = warp_wait_all(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma);
-      const TreeSeg sg_done = sg;
-      sg = nx;
-      if (!ok) continue;
+      if (!(ok = exchange(l_run, all) && warp_wait_all(bar(kTreePVDone), (g - 1) & 1, ab, kErrWaitMma))) break;
       tc_fence_after();
       const float l = (all[0] + all[1]) + (all[2] + all[3]);
       const int v0 = 256 * ch + 128 * lh;  // this thread's 128 of the 512 values
-      if (sg_done.j1 - sg_done.j0 == sg_done.blocks) {
+      if (sg.j1 - sg.j0 == sg.blocks) {
+        // Through P's shared memory, 32 of each thread's values at a time, so that
+        // 64 consecutive bytes of a row leave together: stored by the threads
+        // that hold them, 16 bytes a row, a tile took 8k clk.
         float inv = l != 0.f ? 1.f / l : 0.f;
         if (p.v_scale != nullptr) inv *= __ldg(p.v_scale + (2 * (r % p.H) + 1) * 4 + (v0 >> 7));
-        uint4* dst = reinterpret_cast<uint4*>(p.olat + ((static_cast<int64_t>(sg_done.b) * p.N) * p.H + r) * 512 + v0);
+        uint8_t* const stage = smem + S::P;
+        const int who = static_cast<int>(threadIdx.x) - 64, piece = who & 15, r0 = sg.tile * kTreeRows + 64 * rank;
+        // piece: 16 bytes of one of the four threads' 64 (values 128 (piece / 4) ...)
+        uint8_t* const dst = reinterpret_cast<uint8_t*>(p.olat + (static_cast<int64_t>(sg.b) * p.N * p.H + r0) * 512) +
+                             (piece >> 2) * 256 + (piece & 3) * 16;
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += 32) {
           uint32_t o[32];
           tmem_ld32(tl + 128u * ch + c0, o);
-          if (r < live) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[c0 / 8 + i] =
-                  make_uint4(pack_bf16x2(__uint_as_float(o[8 * i + 0]) * inv, __uint_as_float(o[8 * i + 1]) * inv),
-                             pack_bf16x2(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv),
-                             pack_bf16x2(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv),
-                             pack_bf16x2(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv));
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(stage + row * 256 + (((4 * (2 * ch + lh) + i) ^ (row & 7)) << 4)) =
+                make_uint4(pack_bf16x2(__uint_as_float(o[8 * i + 0]) * inv, __uint_as_float(o[8 * i + 1]) * inv),
+                           pack_bf16x2(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv),
+                           pack_bf16x2(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv),
+                           pack_bf16x2(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv));
+          if (!(ok = meet())) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = (who >> 4) + 16 * i;
+            if (r0 + rr < live)
+              *reinterpret_cast<uint4*>(dst + rr * 1024 + c0 * 2) =
+                  *reinterpret_cast<const uint4*>(stage + rr * 256 + ((piece ^ (rr & 7)) << 4));
           }
+          if (!(ok = meet())) break;
         }
       } else {
-        const int slot = 2 * pair + (sg_done.first ? 0 : 1);
+        const int slot = 2 * pair + (sg.flags & 1 ? 0 : 1);
         const int tr = 64 * rank + row;
         float* dst = p.part_o + static_cast<int64_t>(slot) * kTreeSlotFloats + (v0 / 4 * kTreeRows + tr) * 4;
         if (part == 0) p.part_ml[slot * kTreeRows + tr] = make_float2(m_run, l);
