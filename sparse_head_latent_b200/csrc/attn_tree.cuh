@@ -55,6 +55,12 @@ constexpr int kTreeRows = 128;      // rows of a tile
 constexpr int kTreeBlock = 128;     // keys of a block
 constexpr int kTreeMaxPairs = 74;   // pairs a launch uses at most (148 SMs); the workspace is sized for them
 constexpr int kTreeThreads = 352;
+// What a tile costs a pair besides its blocks, in blocks: Q's loads, the first
+// products with nothing before them, the result. Where there are more tiles than
+// pairs the shares count it: 98 tiles of 4 to 63 blocks took 145 us in shares of
+// equal blocks, 120, 118, 120 and 125 with 2, 3, 4 and 7 added. With fewer tiles
+// every pair has about one run, and counting it would take blocks from none.
+constexpr int kTreeRunCost = 3;
 constexpr int kTreeSlotFloats = kTreeRows * 512;  // one partial tile
 
 struct TreeParams {
@@ -68,7 +74,7 @@ struct TreeParams {
   const int32_t* parents;        // [B][N], or nullptr: a chain
   const float* v_scale;          // [2 H][4], or nullptr: row 2 h + 1 multiplies the four 128s of head h's o_lat
   __nv_bfloat16* olat;           // [B*N][H][512]
-  int64_t* ustart;               // [B + 1] first unit of each sequence, and their number
+  int64_t* ustart;               // [B + 2] first unit of each sequence, their number, and what a tile adds to its blocks
   float* part_o;                 // [2 pairs][128 value quads][128 rows][4] unnormalised partial tiles
   float2* part_ml;               // [2 pairs][128 rows] (max in the scaled log2 domain, sum)
   int* err;
@@ -99,10 +105,10 @@ struct TreeRun {
 
 // Where a pair stands in its share of the units.
 struct TreeWork {
-  int64_t left;                   // units still to walk
+  int64_t left;                   // units still to walk, without the open tile's own
   int b, tile, j;                 // where the next run begins
   int len, nodes, tiles, blocks;  // of sequence b
-  int first;
+  int first, extra;               // units of a tile besides its blocks
   __device__ __forceinline__ TreeRun next(const TreeParams& p) {
     while (tile >= tiles) {
       tree_lengths(p, ++b, len, nodes);
@@ -117,7 +123,7 @@ struct TreeWork {
     r.len = len;
     r.nodes = nodes;
     r.blocks = blocks;
-    left -= r.j1 - j;
+    left -= r.j1 - j + extra;
     r.flags = first | (left > 0 ? 2 : 0);
     first = 0;
     j = 0;
@@ -143,7 +149,7 @@ struct TreeSmem {
   static constexpr int P = Q + Q_CHUNKS * CHUNK;   // two [64 rows x 64 keys] chunks
   static constexpr int XCHG = P + 2 * CHUNK;       // [2][4][64] floats
   static constexpr int BARS = XCHG + 2 * 4 * 64 * 4;
-  static constexpr int START = BARS + 400;         // where the share begins: sequence, tile, block
+  static constexpr int START = BARS + 400;         // where the share begins: sequence, tile, block, extra units
   static constexpr int RUNS = BARS + 416;          // four TreeRuns, published by the producer of keys
   static constexpr int BYTES = RUNS + 4 * 32;
 };
@@ -270,55 +276,66 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
   // a run of sequences.
   TreeWork work;
   {
-    int64_t* sums = reinterpret_cast<int64_t*>(smem + S::XCHG);
+    int64_t* sums = reinterpret_cast<int64_t*>(smem + S::XCHG);  // per warp: blocks, tiles
     const int per = (p.B + kTreeThreads - 1) / kTreeThreads;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-    int64_t mine = 0;
+    int64_t blocks_mine = 0, tiles_mine = 0;
     for (int b = b0; b < b1; ++b) {
       int len, nodes, tiles, blocks;
       tree_lengths(p, b, len, nodes);
       tree_extent(p, len, nodes, tiles, blocks);
-      mine += static_cast<int64_t>(tiles) * blocks;
+      blocks_mine += static_cast<int64_t>(tiles) * blocks;
+      tiles_mine += tiles;
     }
-    int64_t incl = mine;
+    int64_t blocks_to = blocks_mine, tiles_to = tiles_mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int64_t v = __shfl_up_sync(0xffffffffu, blocks_to, o), w = __shfl_up_sync(0xffffffffu, tiles_to, o);
+      if (lane >= o) blocks_to += v, tiles_to += w;
     }
-    if (lane == 31) sums[warp] = incl;
+    if (lane == 31) sums[2 * warp] = blocks_to, sums[2 * warp + 1] = tiles_to;
     __syncthreads();
-    int64_t before = 0, total = 0;
+    int64_t total = 0, tiles_all = 0;
     for (int w = 0; w < kTreeThreads / 32; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
+      if (w < warp) blocks_to += sums[2 * w], tiles_to += sums[2 * w + 1];
+      total += sums[2 * w];
+      tiles_all += sums[2 * w + 1];
     }
-    int64_t at = before + incl - mine;
+    const int extra = tiles_all > pairs ? kTreeRunCost : 0;
+    total += extra * tiles_all;
+    int64_t at = blocks_to - blocks_mine + extra * (tiles_to - tiles_mine);
     const int64_t u0 = tree_share(total, pair, pairs);
-    const bool mark = blockIdx.x == 0, here = u0 >= at && u0 < at + mine;
+    const bool mark = blockIdx.x == 0, here = u0 >= at && u0 < at + blocks_mine + extra * tiles_mine;
     if (mark || here) {
       for (int b = b0; b < b1; ++b) {
         int len, nodes, tiles, blocks;
         tree_lengths(p, b, len, nodes);
         tree_extent(p, len, nodes, tiles, blocks);
-        const int64_t units = static_cast<int64_t>(tiles) * blocks;
+        const int64_t units = static_cast<int64_t>(tiles) * (blocks + extra);
         if (mark) p.ustart[b] = at;
         if (u0 >= at && u0 < at + units) {
+          const int off = static_cast<int>((u0 - at) % (blocks + extra));
           start[0] = b;
-          start[1] = static_cast<int>((u0 - at) / blocks);
-          start[2] = static_cast<int>((u0 - at) % blocks);
+          start[1] = static_cast<int>((u0 - at) / (blocks + extra));
+          start[2] = max(0, off - extra);
+          start[3] = max(0, extra - off);  // of the first run's own units
         }
         at += units;
       }
     }
-    if (mark && threadIdx.x == 0) p.ustart[p.B] = total;
+    if (mark && threadIdx.x == 0) {
+      p.ustart[p.B] = total;
+      p.ustart[p.B + 1] = extra;
+    }
     work.left = tree_share(total, pair + 1, pairs) - u0;
+    work.extra = extra;
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrival
   tc_fence_after();
   griddep_launch();
+  if (work.left > 0) work.left -= start[3];
   const bool busy = work.left > 0;  // the pair has work at all
   const uint32_t tmem = *tmem_slot;
   const Abort ab{abort_word, p.err};
@@ -828,9 +845,12 @@ tree_combine_kernel(const TreeParams p, int pairs) {
   int slot = -1;
   if (c < 96) {
     if (c < pairs && tile < tiles) {
-      const int64_t units = p.ustart[p.B], lo = p.ustart[b] + static_cast<int64_t>(tile) * blocks, hi = lo + blocks;
-      const int64_t s0 = tree_share(units, c, pairs), s1 = tree_share(units, c + 1, pairs);
-      if (s1 > s0 && s1 > lo && s0 < hi && !(s0 <= lo && s1 >= hi)) slot = 2 * c + (s0 >= lo ? 0 : 1);
+      // Its share [s0, s1) as blocks of this tile, counted from the first.
+      const int64_t units = p.ustart[p.B], extra = p.ustart[p.B + 1];
+      const int64_t lo = p.ustart[b] + static_cast<int64_t>(tile) * (blocks + extra) + extra;
+      const int64_t s0 = tree_share(units, c, pairs) - lo, s1 = tree_share(units, c + 1, pairs) - lo;
+      const int64_t j0 = max(s0, int64_t(0)), j1 = min(s1, int64_t(blocks));
+      if (j0 < j1 && j1 - j0 < blocks) slot = 2 * c + (s0 >= -extra ? 0 : 1);
     }
     const uint32_t mine = __ballot_sync(0xffffffffu, slot >= 0);
     if ((c & 31) == 0) found[c >> 5] = static_cast<int>(mine);

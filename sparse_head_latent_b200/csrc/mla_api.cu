@@ -471,7 +471,7 @@ WsLayout ws_layout(const mla_dims& d, int entry, bool has_topk) {
     w.qabs = take(rows * H * kL * 2);
     w.olat = take(rows * H * kL * 2);
     w.attn = take(rows * H * kDv * 2);
-    w.tree_start = take((static_cast<size_t>(d.B) + 1) * 8);
+    w.tree_start = take((static_cast<size_t>(d.B) + 2) * 8);
     w.tree_ml = take(size_t(2) * mla::kTreeMaxPairs * mla::kTreeRows * 8);
     w.tree_o = take(size_t(2) * mla::kTreeMaxPairs * mla::kTreeSlotFloats * 4);
     if (rows <= kFewRows) {
