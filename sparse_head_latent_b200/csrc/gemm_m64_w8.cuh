@@ -4,7 +4,7 @@
 // mla_decode first writes a bf16 copy of W_kvb and W_o: the 134 MB of codes of
 // 128 heads are read, 268 MB written and read again, 89 us before the products
 // begin. Here each CTA's share of the codes goes from HBM to shared memory by
-// TMA and eight warps turn it into the bf16 operand there, so that a weight
+// TMA and sixteen warps turn it into the bf16 operand there, so that a weight
 // costs one byte of HBM traffic. Scales (one per 128 x 128 block):
 //   absorb  (q_nope . W_UK, K = 128): one scale per output tile, applied to the
 //           fp32 accumulator; the codes are exact in bf16
@@ -12,9 +12,9 @@
 //           attention has multiplied into o_lat before rounding it
 //   W_o     (stream-K): bf16(code * scale), rounded once, as the copy would be
 //
-// Roles (480 threads, one CTA per SM): warp 0 asks for codes, warp 14 for A; warp
-// 1 tensor memory and UMMA issuer; warps 2..5 epilogue; warps 6..13 converters,
-// two teams that take tiles in turn. Codes ([64 x 128], 8 KB), A ([BM x 64]) and
+// Roles (736 threads, one CTA per SM): warp 0 asks for codes, warp 22 for A; warp
+// 1 tensor memory and UMMA issuer; warps 2..5 epilogue; warps 6..21 converters,
+// four teams that take tiles in turn. Codes ([64 x 128], 8 KB), A ([BM x 64]) and
 // converted operands (16 KB) have rings of their own: with a common stage, five
 // to seven of which fit, only 40 to 56 KB of codes were in flight per SM, and W_o's
 // 117 MB took 53 us. Work (segments, stream-K shares, batches) as in
@@ -43,6 +43,7 @@ struct GemmM64W8Cfg {
   static constexpr int SMEM_BYTES = 1024 + BARS + NUM_BARS * 8 + 16;
   static constexpr uint32_t TMEM_COLS = 256;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(BUFS % TEAMS == 0 && W_STAGES >= BUFS, "a team has buffers of its own; see its first wait");
 };
 
 // Two e4m3 codes to two bf16, times s if SCALED (fp32 product, one rounding;
@@ -197,15 +198,18 @@ gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         const int s = it % SW, b = it % NB;
         float f = 1.f;
         if constexpr (!Cfg::BATCH) f = __ldg(scale + static_cast<int64_t>(kb >> 1) * (N / 128) + sg.nt);
+        // The buffer first: once the product four tiles before is done with it, all
+        // codes up to that tile have landed, the lap before of this stage among
+        // them. A stage is taken by two teams in turn and loads land in any
+        // order, so the other way round the parity of two laps before could
+        // let a team through to old codes.
+        if (!(ok = warp_wait_all(bempty0 + 8 * b, ((it / NB) & 1) ^ 1, ab, kErrWaitMma))) break;
         if (!(ok = warp_wait_all(wfull0 + 8 * s, (it / SW) & 1, ab, kErrWaitTma))) break;
         const uint8_t* src = smem + Cfg::W0 + s * Cfg::W_BYTES;
         uint4 w[PIECES];
 #pragma unroll
         for (int i = 0; i < PIECES; ++i)
           w[i] = *reinterpret_cast<const uint4*>(src + (me + i * 32 * Cfg::TEAM) * 16);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(wempty0 + 8 * s);
-        if (!(ok = warp_wait_all(bempty0 + 8 * b, ((it / NB) & 1) ^ 1, ab, kErrWaitMma))) break;
         uint8_t* dst = smem + Cfg::BUF0 + b * Cfg::BUF_BYTES;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
@@ -222,9 +226,15 @@ gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
           *reinterpret_cast<uint4*>(d + (((2 * q) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<uint4*>(d + (((2 * q + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
+        // For the stores, which the tensor core reads, and the loads of the codes,
+        // whose stage TMA writes again: without it before the stage's release,
+        // loads came after that write, in a tile or so per call.
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bfull0 + 8 * b);
+        if (lane == 0) {
+          mbar_arrive(bfull0 + 8 * b);
+          mbar_arrive(wempty0 + 8 * s);
+        }
       }
     }
   } else {

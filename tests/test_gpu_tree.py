@@ -308,6 +308,18 @@ def test_many_runs_of_blocks_per_pair(N, H, page):
     assert_near(first[some], p.expect(some)[some])
 
 
+@pytest.mark.parametrize("B,N,H", [(5, 1, 128), (8, 8, 64), (16, 8, 128), (50, 5, 128), (13, 5, 3)])
+def test_e4m3_codes_read_as_stored_give_the_same_result_every_time(B, N, H):
+    # rows of one, of 64 or fewer, of two tiles of 128: codes in flight for every head and all of W_o
+    p = Problem([40 + 7 * b for b in range(B)], N, H, page=32, fp8=True)
+    first = p.run()
+    for _ in range(10):
+        assert torch.equal(p.run(), first)
+    _no_device_error()
+    some = sorted({0, B // 2, B - 1})
+    assert_near(first[some], p.expect(some)[some])
+
+
 def test_captured_graph_follows_its_inputs():
     p = Problem([500, 900], 4, 8)
     n0, nodes, table = p.i32(p.lens), p.i32(p.nodes), p.table.clone()
