@@ -507,6 +507,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       bool ok = true;
       int g = 0, seg = 0, commits = 0;
       uint32_t ks = 0, kparity = 0, vs = 0, vparity = 0;  // the next groups of keys and of values
+      griddep_wait();                                     // no bounded wait begins before that
       auto qk = [&](int block) -> bool {
         constexpr int kChunk = S::CHUNK >> 4, kGroup = S::GROUP >> 4;
         const uint32_t ts = tmem + kTreeColS;
@@ -633,6 +634,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       if (lane == 0) mbar_arrive_remote(mapa_shared(bar(kTreeQReady), 0));
       return true;
     };
+    griddep_wait();
     if (busy) ok = load_q(0);
     bool more = busy;
     while (ok && more) {

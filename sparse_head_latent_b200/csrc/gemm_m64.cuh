@@ -208,6 +208,7 @@ gemm_m64_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       constexpr uint32_t idesc = idesc_bf16_f32(Cfg::BM, Cfg::BN, 0, Cfg::B_MN_MAJOR ? 1 : 0);
       int it = 0, t = 0;
       bool ok = true;
+      griddep_wait();
       for (; ok && work.next(sg); ++t) {
         const int a = t & 1;
         if (!mbar_wait(acce0 + 8 * a, ((t >> 1) & 1) ^ 1, ab, kErrWaitEpilogue)) {
@@ -247,6 +248,7 @@ gemm_m64_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     constexpr int RPW = Cfg::BM / 4;  // rows per warp
     const int q = warp & 3;
     int t = 0;
+    griddep_wait();  // no bounded wait begins before that
     for (; work.next(sg); ++t) {
       const int mt = sg.mt, nt = sg.nt, sp = sg.z;
       const int a = t & 1;

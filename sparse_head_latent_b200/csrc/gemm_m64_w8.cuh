@@ -126,7 +126,7 @@ gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       const int stages = codes ? SW : SA;
       int s = 0;
       uint32_t parity = 1;
-      bool ok = true;
+      bool ok = true, waited = !codes;
       while (ok && work.next(sg)) {
         const int wrow = bt.b_row0 + sg.z * bt.b_step;
         for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
@@ -143,7 +143,11 @@ gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             tma_load_2d(dst, &tmW, fb, sg.nt * Cfg::BN, wrow + k);
           else
             tma_load_2d(dst, &tmW, fb, k, wrow + sg.nt * Cfg::BN);
-          if (++s == stages) s = 0, parity ^= 1;
+          if (++s == stages) {
+            s = 0, parity ^= 1;
+            if (!waited) griddep_wait();  // the next lap's stages come free behind A's first tiles
+            waited = true;
+          }
         }
       }
       if (!ok) spin_ns(2000000);  // let issued loads land before the CTA can exit
@@ -157,6 +161,7 @@ gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     uint32_t s = 0, sp = 0, b = 0, bp = 0;
     int t = 0, last = -1;
     bool ok = true;
+    griddep_wait();
     for (; ok && work.next(sg); ++t) {
       const int a = t & 1;
       if (!mbar_wait_short(acce0 + 8 * a, ((t >> 1) & 1) ^ 1, ab, kErrWaitEpilogue)) break;
@@ -195,6 +200,7 @@ gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 #pragma unroll 1
       for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
         if (it % Cfg::TEAMS != team) continue;
+        if (it / NB == 1) griddep_wait();  // from here on a buffer comes free behind A's tiles
         const int s = it % SW, b = it % NB;
         float f = 1.f;
         if constexpr (!Cfg::BATCH) f = __ldg(scale + static_cast<int64_t>(kb >> 1) * (N / 128) + sg.nt);
@@ -243,6 +249,7 @@ gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     constexpr int RPW = Cfg::BM / 4;  // rows per warp
     const int q = warp & 3;
     int t = 0;
+    griddep_wait();
     for (; work.next(sg); ++t) {
       const int a = t & 1;
       float f = 1.f;
