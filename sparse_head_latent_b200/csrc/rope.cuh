@@ -28,6 +28,14 @@ struct RopeTable {
   int layout;                  // MLA_ROPE_INTERLEAVED or MLA_ROPE_HALF
 };
 
+// The table's frequencies by a generic address: as a constant each lane's own
+// index would be read one after the other.
+__device__ __forceinline__ const uint64_t* rope_turns(const RopeTable& tab) {
+  const uint64_t* t = tab.turns;
+  asm("" : "+l"(t));
+  return t;
+}
+
 // m cos and m sin of position * f, the sine negated for the inverse.
 __device__ __forceinline__ float2 rope_cos_sin(int position, uint64_t turns, float magnitude, bool inverse) {
   const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(position)) * turns;
@@ -66,7 +74,8 @@ constexpr int kRopeThreads = 256;
 // inside it is rotated with four cosines and sines that the thread computes
 // once for its row and uses for all its heads. With many heads a block covers
 // heads_per_block heads of one row, with few it covers several rows. Four
-// heads are loaded before the first is stored, to keep loads in flight.
+// heads are loaded before the first is stored, to keep loads in flight. 4096
+// rows of 128 heads of 192, 403 MB: 62.5 us, 6.4 TB/s; one row of 64 heads: 2 us.
 template <bool HALF>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const __grid_constant__ RopeTable tab, const RopeParams p) {
@@ -112,10 +121,15 @@ rope_kernel(const __grid_constant__ RopeTable tab, const RopeParams p) {
   };
   load();  // in flight while the cosines are made
   float2 cs[4];
+  uint64_t turns[4];
+  if (turn) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turns[i] = rope_turns(tab)[4 * k + i];
+  }
   if (turn) {
     const int pos = __ldg(p.positions + row);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = rope_cos_sin(pos, tab.turns[4 * k + i], tab.magnitude, p.inverse);
+    for (int i = 0; i < 4; ++i) cs[i] = rope_cos_sin(pos, turns[i], tab.magnitude, p.inverse);
   }
   while (h < h_end) {
 #pragma unroll
@@ -169,7 +183,10 @@ struct AppendParams {
 // One warp per token: c = w x / sqrt(mean x^2 + eps) over the 512 latent
 // values (16 a lane, the sum in fp32 by shuffles) and the rotated key (one
 // pair a lane), each rounded once, into the token's cache row. A token whose
-// slot lies outside the cache is skipped.
+// slot lies outside the cache is skipped. 16384 tokens, 38 MB: 9.9 us; 65536:
+// 32 us, 4.7 TB/s. Four tokens a warp, all loaded first, took 13.4 us, a warp that
+// loads its next token while it works on one 11.5: at 48 registers ten blocks
+// share an SM, and that hides more.
 template <bool HALF>
 __global__ void __launch_bounds__(128)
 cache_append_kernel(const __grid_constant__ RopeTable tab, const AppendParams p) {
@@ -177,6 +194,7 @@ cache_append_kernel(const __grid_constant__ RopeTable tab, const AppendParams p)
   const int row = static_cast<int>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (row >= p.rows) return;
   // Everything is loaded before anything is looked at.
+  const uint64_t turns = rope_turns(tab)[lane];
   const int64_t slot = p.slots ? __ldg(p.slots + row) : row;
   const int pos = __ldg(p.positions + row);
   const __nv_bfloat16* src = p.kv_a + row * p.kv_row;
@@ -238,7 +256,7 @@ cache_append_kernel(const __grid_constant__ RopeTable tab, const AppendParams p)
     dst[lane + 32 * i] = make_uint4(o[0], o[1], o[2], o[3]);
   }
   float a, b;
-  rope_turn(u, v, rope_cos_sin(pos, tab.turns[lane], tab.magnitude, false), a, b);
+  rope_turn(u, v, rope_cos_sin(pos, turns, tab.magnitude, false), a, b);
   __nv_bfloat16* kd = p.pe + slot * 64;
   if (HALF) {
     kd[lane] = __float2bfloat16_rn(a);
