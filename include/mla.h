@@ -387,8 +387,11 @@ int mla_cache_append(const mla_rope_table* table, const void* kv_a, long long kv
  * lies outside [0, num_pages): that sequence's out rows are undefined (nothing
  * outside the caches is read); 402 cache_len < 0 or cache_len + n_nodes beyond
  * the table: that sequence's out rows are 0.
+ * e4m3 weights are read as stored up to 256 rows (B N); more rows go through
+ * bf16 copies in the workspace.
  * Workspace: mla_workspace_bytes(dims, MLA_ENTRY_TREE_DECODE, 0).
- * Errors: as for mla_decode; MLA_ERR_SHAPE also for bad pages or N. */
+ * Errors: as for mla_decode; MLA_ERR_SHAPE also for bad pages or N, and for
+ * B N H beyond 2^27. */
 int mla_tree_decode(const mla_dims* dims, const mla_pages* pages, const void* q, const void* kv_cache,
                     const void* k_pe_cache, const int32_t* block_table, const int32_t* cache_len,
                     const int32_t* n_nodes, const int32_t* parents, const void* W_kvb, const float* W_kvb_scale,

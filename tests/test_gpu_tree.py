@@ -350,6 +350,49 @@ def test_captured_graph_follows_its_inputs():
 # ------------------------------------------------------------------ upkeep
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_two_graphs_share_a_workspace(fp8):
+    # one step each of two models' batches, replayed in turn on one stream
+    a, b = Problem([700, 90, 3000], 3, 16, fp8=fp8), Problem([64, 2000, 5], 3, 16, fp8=fp8, seed=9)
+    ws = torch.empty(mla.mla_workspace_bytes(mla.make_dims(3, 3, 16, fp8=fp8), mla.MLA_ENTRY_TREE_DECODE, False),
+                     dtype=torch.uint8, device="cuda")
+    want = [p.run() for p in (a, b)]
+    graphs, outs = [], []
+    for p in (a, b):
+        n0, nodes = p.i32(p.lens), p.i32(p.nodes)
+        out = torch.empty(3, 3, 7168, dtype=torch.bfloat16, device="cuda")
+        call = lambda: p.run(cache_len=n0, n_nodes=nodes, out=out, workspace=ws)  # noqa: B023, E731
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graphs.append((graph, n0, nodes))
+        outs.append(out)
+    for _ in range(3):
+        for out in outs:
+            out.zero_()
+        for graph, _, _ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    _no_device_error()
+
+
+def test_e4m3_calls_on_two_streams_at_once():
+    problems = [Problem([300 + 50 * b for b in range(12)], 7, 128, fp8=True, seed=s) for s in (1, 2)]
+    want = [p.run() for p in problems]
+    streams = [torch.cuda.Stream() for _ in problems]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    args = [dict(cache_len=p.i32(p.lens), n_nodes=p.i32(p.nodes)) for p in problems]
+    torch.cuda.synchronize()
+    got = [[p.run(stream=st, **a) for _ in range(6)] for p, st, a in zip(problems, streams, args)]
+    torch.cuda.synchronize()
+    _no_device_error()
+    for outs, w in zip(got, want):
+        assert all(torch.equal(o, w) for o in outs)
+
+
 def _caches(layers, pages, page, seed=0):
     g = torch.Generator(device="cuda").manual_seed(seed)
     shape = (pages, page) if layers is None else (layers, pages, page)
