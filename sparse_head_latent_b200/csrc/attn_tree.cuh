@@ -131,8 +131,13 @@ struct TreeWork {
   }
 };
 
-__host__ __device__ __forceinline__ int64_t tree_share(int64_t units, int pair, int pairs) {
-  return units * pair / pairs;
+// First units of the shares of `pair` and of the next: equal, the first
+// units % pairs of them one longer. One division, of 64 bits: a few hundred
+// clk, on the way to a block's first load.
+__device__ __forceinline__ void tree_share(int64_t units, int pair, int pairs, int64_t& u0, int64_t& u1) {
+  const int64_t each = units / pairs, more = units - each * pairs;
+  u0 = each * pair + (pair < more ? pair : more);
+  u1 = u0 + each + (pair < more ? 1 : 0);
 }
 
 struct TreeSmem {
@@ -254,12 +259,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
   const int rank = static_cast<int>(cluster_ctarank());
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kTreeBars; ++i) {
-      const bool both = i == kTreeSFree || i == kTreePFull || i == kTreeQReady;
-      mbar_init(bar(i), both ? 16 : i == kTreeOut ? 8 : i == kTreeXchg || i == kTreeXchg + 1 ? 4 : 1);
-    }
-    *abort_word = 0;
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + kTreeBars) {
+    const int i = static_cast<int>(threadIdx.x) - 64;
+    const bool both = i == kTreeSFree || i == kTreePFull || i == kTreeQReady;
+    mbar_init(bar(i), both ? 16 : i == kTreeOut ? 8 : i == kTreeXchg || i == kTreeXchg + 1 ? 4 : 1);
+    if (i == 0) *abort_word = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -279,7 +283,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
     int64_t* sums = reinterpret_cast<int64_t*>(smem + S::XCHG);  // per warp: blocks, tiles
     const int per = (p.B + kTreeThreads - 1) / kTreeThreads;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-    int64_t blocks_mine = 0, tiles_mine = 0;
+    int64_t blocks_mine = 0;
+    int tiles_mine = 0;  // 2^28 in all at most
     for (int b = b0; b < b1; ++b) {
       int len, nodes, tiles, blocks;
       tree_lengths(p, b, len, nodes);
@@ -287,25 +292,28 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       blocks_mine += static_cast<int64_t>(tiles) * blocks;
       tiles_mine += tiles;
     }
-    int64_t blocks_to = blocks_mine, tiles_to = tiles_mine;
+    int64_t blocks_to = blocks_mine;
+    int tiles_to = tiles_mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, blocks_to, o), w = __shfl_up_sync(0xffffffffu, tiles_to, o);
+      const int64_t v = __shfl_up_sync(0xffffffffu, blocks_to, o);
+      const int w = __shfl_up_sync(0xffffffffu, tiles_to, o);
       if (lane >= o) blocks_to += v, tiles_to += w;
     }
     if (lane == 31) sums[2 * warp] = blocks_to, sums[2 * warp + 1] = tiles_to;
     __syncthreads();
     int64_t total = 0, tiles_all = 0;
     for (int w = 0; w < kTreeThreads / 32; ++w) {
-      if (w < warp) blocks_to += sums[2 * w], tiles_to += sums[2 * w + 1];
+      if (w < warp) blocks_to += sums[2 * w], tiles_to += static_cast<int>(sums[2 * w + 1]);
       total += sums[2 * w];
       tiles_all += sums[2 * w + 1];
     }
     const int extra = tiles_all > pairs ? kTreeRunCost : 0;
     total += extra * tiles_all;
-    int64_t at = blocks_to - blocks_mine + extra * (tiles_to - tiles_mine);
-    const int64_t u0 = tree_share(total, pair, pairs);
-    const bool mark = blockIdx.x == 0, here = u0 >= at && u0 < at + blocks_mine + extra * tiles_mine;
+    int64_t at = blocks_to - blocks_mine + static_cast<int64_t>(extra) * (tiles_to - tiles_mine);
+    int64_t u0, u1;
+    tree_share(total, pair, pairs, u0, u1);
+    const bool mark = blockIdx.x == 0, here = u0 >= at && u0 < at + blocks_mine + static_cast<int64_t>(extra) * tiles_mine;
     if (mark || here) {
       for (int b = b0; b < b1; ++b) {
         int len, nodes, tiles, blocks;
@@ -314,9 +322,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         const int64_t units = static_cast<int64_t>(tiles) * (blocks + extra);
         if (mark) p.ustart[b] = at;
         if (u0 >= at && u0 < at + units) {
-          const int off = static_cast<int>((u0 - at) % (blocks + extra));
+          const int64_t tile = (u0 - at) / (blocks + extra);
+          const int off = static_cast<int>(u0 - at - tile * (blocks + extra));
           start[0] = b;
-          start[1] = static_cast<int>((u0 - at) / (blocks + extra));
+          start[1] = static_cast<int>(tile);
           start[2] = max(0, off - extra);
           start[3] = max(0, extra - off);  // of the first run's own units
         }
@@ -327,7 +336,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
       p.ustart[p.B] = total;
       p.ustart[p.B + 1] = extra;
     }
-    work.left = tree_share(total, pair + 1, pairs) - u0;
+    work.left = u1 - u0;
     work.extra = extra;
   }
   tc_fence_before();
@@ -822,8 +831,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
 // are not there. Thread: one row of a tile, 16 of its values; with M the
 // largest of the parts' maxima, o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p
 // over the pairs p whose shares meet the tile, in their order. The pairs are
-// found side by side, one per thread: each takes two 64-bit divisions, which in
-// a row took 40 us for a tile of eight parts.
+// found side by side, one per thread: one after the other, with their 64-bit
+// divisions, took 40 us for a tile of eight parts.
 constexpr int kTreeJoinThreads = 256;
 constexpr int kTreeJoinBlocks = kTreeRows * 32 / kTreeJoinThreads;  // per tile
 static_assert(kTreeMaxPairs <= 96, "three warps look for the parts");
@@ -850,7 +859,9 @@ tree_combine_kernel(const TreeParams p, int pairs) {
       // Its share [s0, s1) as blocks of this tile, counted from the first.
       const int64_t units = p.ustart[p.B], extra = p.ustart[p.B + 1];
       const int64_t lo = p.ustart[b] + static_cast<int64_t>(tile) * (blocks + extra) + extra;
-      const int64_t s0 = tree_share(units, c, pairs) - lo, s1 = tree_share(units, c + 1, pairs) - lo;
+      int64_t s0, s1;
+      tree_share(units, c, pairs, s0, s1);
+      s0 -= lo, s1 -= lo;
       const int64_t j0 = max(s0, int64_t(0)), j1 = min(s1, int64_t(blocks));
       if (j0 < j1 && j1 - j0 < blocks) slot = 2 * c + (s0 >= -extra ? 0 : 1);
     }
