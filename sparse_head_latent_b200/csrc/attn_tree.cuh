@@ -848,6 +848,8 @@ tree_combine_kernel(const TreeParams p, int pairs) {
   const int item = static_cast<int>(blockIdx.x) % kTreeJoinBlocks * kTreeJoinThreads + static_cast<int>(threadIdx.x);
   const int tr = item & 127, v0 = (item >> 7) * 16;
   const int r = tile * kTreeRows + tr;
+  // Asked for before the lengths are looked at.
+  const int64_t units = p.ustart[p.B], extra = p.ustart[p.B + 1], first = p.ustart[b];
   int len, nodes, tiles, blocks;
   tree_lengths(p, b, len, nodes);
   tree_extent(p, len, nodes, tiles, blocks);
@@ -857,8 +859,7 @@ tree_combine_kernel(const TreeParams p, int pairs) {
   if (c < 96) {
     if (c < pairs && tile < tiles) {
       // Its share [s0, s1) as blocks of this tile, counted from the first.
-      const int64_t units = p.ustart[p.B], extra = p.ustart[p.B + 1];
-      const int64_t lo = p.ustart[b] + static_cast<int64_t>(tile) * (blocks + extra) + extra;
+      const int64_t lo = first + static_cast<int64_t>(tile) * (blocks + extra) + extra;
       int64_t s0, s1;
       tree_share(units, c, pairs, s0, s1);
       s0 -= lo, s1 -= lo;
