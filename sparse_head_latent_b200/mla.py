@@ -295,46 +295,60 @@ def mla_quantize_act(x, codes=None, scales=None, stream=None):
 # ------------------------------------------------------------------ serving over a paged cache
 
 
-# These calls take a few microseconds on the device at the smallest sizes, so their host side is kept short.
+# These calls take two microseconds on the device at the smallest sizes, so their host side is kept short: tensors are
+# asked for few attributes, and for none twice.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream's handle without its object
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_BF16, _I32 = torch.bfloat16, torch.int32
 
 
 def _expect(t, name, dtype, shape=None):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-def _call(name, device, stream, args, used=()):
-    """Runs an entry point on the tensors' device, on `stream` or that device's current stream. `used`: tensors
-    allocated here, which the caching allocator must not hand out again before `stream` is done with them."""
-    if device.type != "cuda":
+def _cuda(t):
+    """Index of the tensor's CUDA device."""
+    index = t.get_device()
+    if index < 0:
         raise ValueError("tensor must be on a CUDA device")
+    return index
+
+
+def _data(t, index, strided=False):
+    """Address of a tensor that has to be on CUDA device `index` and, unless `strided`, contiguous; None for None."""
+    if t is None:
+        return None
+    if t.get_device() != index:
+        raise ValueError(f"the tensors are on cuda:{index} and {t.device}")
+    if not (strided or t.is_contiguous()):
+        raise ValueError("tensor must be contiguous")
+    return t.data_ptr()
+
+
+def _call(name, index, stream, args, used=()):
+    """Runs an entry point on CUDA device `index`, on `stream` or that device's current stream. `used`: tensors
+    allocated here, which the caching allocator must not hand out again before `stream` is done with them."""
     fn = getattr(_lib or load_library(), name)
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        if stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
         for t in used:
             t.record_stream(stream)
         handle = stream.cuda_stream
     elif _raw_stream is not None:
-        handle = _raw_stream(device.index)
+        handle = _raw_stream(index)
     else:
-        handle = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
+        handle = torch.cuda.current_stream(index).cuda_stream
+    if index == _current_device():
         rc = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, handle)
     if rc != 0:
         raise MlaError(name, rc)
-
-
-def _same_device(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"the tensors are on {device} and {t.device}")
 
 
 def make_rope(base=10000.0, layout=MLA_ROPE_INTERLEAVED, scaling=MLA_ROPE_UNSCALED, factor=1.0, original_len=4096,
@@ -348,17 +362,17 @@ def make_rope(base=10000.0, layout=MLA_ROPE_INTERLEAVED, scaling=MLA_ROPE_UNSCAL
     return table
 
 
-def _rows_and_heads(t, lead):
+def _rows_and_heads(t, shape, lead):
     """(rows, row stride, heads, head stride) of a tensor [*lead, H, W] or [*lead, W] whose last dimension is
     contiguous and whose leading ones fold into one."""
-    shape = t.shape
     n = len(shape)
     if n != lead + 1 and n != lead + 2:
         raise ValueError("the tensor must be [*positions.shape, heads, width] or [*positions.shape, width]")
+    width = shape[-1]
     heads = shape[-2] if n == lead + 2 else 1
     if t.is_contiguous():
-        row = heads * shape[-1]
-        return (t.numel() // row if row else 0), row, heads, shape[-1]
+        row = heads * width
+        return (t.numel() // row if row else 0), row, heads, width
     strides = t.stride()
     if strides[-1] != 1:
         raise ValueError("the tensor's last dimension must be contiguous")
@@ -371,7 +385,7 @@ def _rows_and_heads(t, lead):
         elif strides[d] != row * rows:
             raise ValueError("the leading dimensions must fold into one")
         rows *= shape[d]
-    return rows, row, heads, strides[-2] if n == lead + 2 else shape[-1]
+    return rows, row, heads, strides[-2] if n == lead + 2 else width
 
 
 def mla_rope(x, positions, rope, offset=None, out=None, inverse=False, stream=None):
@@ -379,25 +393,27 @@ def mla_rope(x, positions, rope, offset=None, out=None, inverse=False, stream=No
     positions int32; elements [offset, offset + 64) (default: the last 64) are turned, the others copied. `out` may be
     x (in place). Strided x and out are taken as they are. inverse=True rotates back (the transposed map: with
     x = d out, the gradient). `rope` comes from make_rope."""
-    _expect(x, "x", torch.bfloat16)
-    _expect(positions, "positions", torch.int32)
-    shape, device = x.shape, x.device
-    lead = positions.dim()
-    rows, x_row, heads, x_head = _rows_and_heads(x, lead)
-    if shape[:lead] != positions.shape:
-        raise ValueError(f"x {tuple(shape)} does not start with the shape of positions {tuple(positions.shape)}")
+    if not (x.dtype is _BF16 and positions.dtype is _I32):
+        raise ValueError("x must be torch.bfloat16 and positions torch.int32")
+    shape, at = x.shape, positions.shape
+    lead = len(at)
+    rows, x_row, heads, x_head = _rows_and_heads(x, shape, lead)
+    if shape[:lead] != at:
+        raise ValueError(f"x {tuple(shape)} does not start with the shape of positions {tuple(at)}")
+    index = _cuda(x)
     used = ()
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        out = torch.empty(shape, dtype=_BF16, device=x.device)
         used = (out,)
-    elif out is not x:
-        _expect(out, "out", torch.bfloat16, shape)
-    _same_device(device, positions, out)
-    _, o_row, _, o_head = _rows_and_heads(out, lead)
+    if out is x:
+        o_row, o_head = x_row, x_head
+    else:
+        _expect(out, "out", _BF16, shape)
+        _, o_row, _, o_head = _rows_and_heads(out, shape, lead)
     width = shape[-1]
-    _call("mla_rope", device, stream,
-          (ctypes.byref(rope), x.data_ptr(), x_row, x_head, out.data_ptr(), o_row, o_head, rows, heads, width,
-           width - D_ROPE if offset is None else int(offset), _ptr(positions), 1 if inverse else 0), used)
+    _call("mla_rope", index, stream,
+          (ctypes.byref(rope), x.data_ptr(), x_row, x_head, _data(out, index, True), o_row, o_head, rows, heads, width,
+           width - D_ROPE if offset is None else int(offset), _data(positions, index), 1 if inverse else 0), used)
     return out
 
 
@@ -406,43 +422,44 @@ def mla_cache_append(kv_a, norm_weight, positions, rope, kv_cache, k_pe_cache, s
     strided), norm_weight bf16 or float32 [512], positions int32; slots int32, one cache row per token (-1: skip), or
     None: token r to row r. kv_cache bf16 [..., 512] and k_pe_cache bf16 [..., 64] are contiguous with the same number
     of rows (pages [P, page, 512], or mla_prefill's kv_latent [B, T, 512]). Returns (kv_cache, k_pe_cache)."""
-    _expect(kv_a, "kv_a", torch.bfloat16)
-    _expect(positions, "positions", torch.int32)
-    _expect(kv_cache, "kv_cache", torch.bfloat16)
-    _expect(k_pe_cache, "k_pe_cache", torch.bfloat16)
-    f32 = norm_weight.dtype == torch.float32
-    if not (f32 or norm_weight.dtype == torch.bfloat16) or norm_weight.shape != (D_LATENT,):
+    if not (kv_a.dtype is kv_cache.dtype is k_pe_cache.dtype is _BF16 and positions.dtype is _I32):
+        raise ValueError("kv_a, kv_cache and k_pe_cache must be torch.bfloat16 and positions torch.int32")
+    f32 = norm_weight.dtype is torch.float32
+    if not (f32 or norm_weight.dtype is _BF16) or norm_weight.shape != (D_LATENT,):
         raise ValueError("norm_weight must be bf16 or float32 [512]")
-    if kv_a.shape[:-1] != positions.shape or kv_a.shape[-1] != D_LATENT + D_ROPE:
+    shape, at = kv_a.shape, positions.shape
+    if shape != (*at, D_LATENT + D_ROPE):
         raise ValueError("kv_a must be [*positions.shape, 576]")
-    rows, stride, _, _ = _rows_and_heads(kv_a, positions.dim())
+    rows, stride, _, _ = _rows_and_heads(kv_a, shape, len(at))
     if rows <= 1:
         stride = D_LATENT + D_ROPE
     if slots is not None:
-        _expect(slots, "slots", torch.int32, positions.shape)
-    if kv_cache.shape[-1] != D_LATENT or k_pe_cache.shape[-1] != D_ROPE or kv_cache.shape[:-1] != k_pe_cache.shape[:-1]:
+        _expect(slots, "slots", _I32, at)
+    latent = kv_cache.shape
+    if latent[-1] != D_LATENT or k_pe_cache.shape != (*latent[:-1], D_ROPE):
         raise ValueError("kv_cache must be [..., 512] and k_pe_cache [..., 64] over the same rows")
     cache_rows = kv_cache.numel() // D_LATENT
     if slots is None and cache_rows < rows:
         raise ValueError("the cache has fewer rows than there are tokens")
-    device = kv_a.device
-    _same_device(device, norm_weight, positions, slots, kv_cache, k_pe_cache)
-    _call("mla_cache_append", device, stream,
-          (ctypes.byref(rope), kv_a.data_ptr(), stride, _ptr(norm_weight), 1 if f32 else 0, float(eps), _ptr(positions), _ptr(slots), rows,
-           _ptr(kv_cache), _ptr(k_pe_cache), cache_rows))
+    index = _cuda(kv_a)
+    _call("mla_cache_append", index, stream,
+          (ctypes.byref(rope), kv_a.data_ptr(), stride, _data(norm_weight, index), 1 if f32 else 0, float(eps),
+           _data(positions, index), _data(slots, index), rows, _data(kv_cache, index), _data(k_pe_cache, index),
+           cache_rows))
     return kv_cache, k_pe_cache
 
 
 def _pages(kv_cache, k_pe_cache, table_width, one_layer):
-    _expect(kv_cache, "kv_cache", torch.bfloat16)
-    _expect(k_pe_cache, "k_pe_cache", torch.bfloat16)
+    if not kv_cache.dtype is k_pe_cache.dtype is _BF16:
+        raise ValueError("kv_cache and k_pe_cache must be torch.bfloat16")
     shape = kv_cache.shape
-    if len(shape) not in ((3,) if one_layer else (3, 4)) or shape[-1] != D_LATENT:
+    n = len(shape)
+    if (n != 3 and (one_layer or n != 4)) or shape[-1] != D_LATENT:
         raise ValueError("kv_cache must be [pages, page_size, 512]" +
                          ("" if one_layer else " or [layers, pages, page_size, 512]"))
-    if k_pe_cache.shape[-1] != D_ROPE or k_pe_cache.shape[:-1] != shape[:-1]:
+    if k_pe_cache.shape != (*shape[:-1], D_ROPE):
         raise ValueError("k_pe_cache must be [..., 64] over kv_cache's pages")
-    return MlaPages(shape[-3], shape[-2], table_width, shape[0] if len(shape) == 4 else 1)
+    return MlaPages(shape[-3], shape[-2], table_width, shape[0] if n == 4 else 1)
 
 
 def mla_tree_decode(q, kv_cache, k_pe_cache, block_table, cache_len, W_kvb, W_o, W_kvb_scale=None, W_o_scale=None,
@@ -475,8 +492,7 @@ def mla_tree_decode(q, kv_cache, k_pe_cache, block_table, cache_len, W_kvb, W_o,
                 raise ValueError(f"e4m3 weights need {name}")
             _expect(s, name, torch.float32, (w.shape[0] // 128, w.shape[1] // 128))
     pages = _pages(kv_cache, k_pe_cache, block_table.shape[1], True)
-    _same_device(q.device, kv_cache, k_pe_cache, block_table, cache_len, W_kvb, W_o, W_kvb_scale, W_o_scale, parents,
-                 n_nodes, out, workspace)
+    index = _cuda(q)
     dims = make_dims(B, N, H, 0, fp8)
     used = []
     if out is None:
@@ -488,10 +504,11 @@ def mla_tree_decode(q, kv_cache, k_pe_cache, block_table, cache_len, W_kvb, W_o,
     ws, nbytes = _workspace(dims, MLA_ENTRY_TREE_DECODE, False, workspace, q.device)
     if own_ws:
         used.append(ws)
-    _call("mla_tree_decode", q.device, stream,
-          (ctypes.byref(dims), ctypes.byref(pages), _ptr(q), _ptr(kv_cache), _ptr(k_pe_cache), _ptr(block_table),
-           _ptr(cache_len), _ptr(n_nodes), _ptr(parents), _ptr(W_kvb), _ptr(W_kvb_scale), _ptr(W_o), _ptr(W_o_scale),
-           float(scale), _ptr(out), _ptr(ws), nbytes), used)
+    _call("mla_tree_decode", index, stream,
+          (ctypes.byref(dims), ctypes.byref(pages), _data(q, index), _data(kv_cache, index), _data(k_pe_cache, index),
+           _data(block_table, index), _data(cache_len, index), _data(n_nodes, index), _data(parents, index),
+           _data(W_kvb, index), _data(W_kvb_scale, index), _data(W_o, index), _data(W_o_scale, index), float(scale),
+           _data(out, index), _data(ws, index), nbytes), used)
     return out
 
 
@@ -499,19 +516,19 @@ def mla_cache_compact(kv_cache, k_pe_cache, block_table, cache_len, accepted, n_
     """Moves each sequence's accepted rows together: position cache_len + accepted[b, i] to cache_len + i for
     i < n_accepted[b], in every layer. kv_cache [pages, page_size, 512] or [layers, pages, page_size, 512] (k_pe_cache
     alike with 64), accepted int32 [B, width <= 64], the others int32 [B]."""
-    pages = _pages(kv_cache, k_pe_cache, block_table.shape[-1], False)
-    _expect(block_table, "block_table", torch.int32)
-    _expect(accepted, "accepted", torch.int32)
-    if block_table.dim() != 2 or accepted.dim() != 2:
+    if not (block_table.dtype is accepted.dtype is cache_len.dtype is n_accepted.dtype is _I32):
+        raise ValueError("block_table, cache_len, accepted and n_accepted must be torch.int32")
+    table, nodes = block_table.shape, accepted.shape
+    if len(table) != 2 or len(nodes) != 2 or table[0] != nodes[0]:
         raise ValueError("block_table and accepted must be [B, width]")
-    B = block_table.shape[0]
-    _expect(cache_len, "cache_len", torch.int32, (B,))
-    _expect(accepted, "accepted", torch.int32, (B, accepted.shape[1]))
-    _expect(n_accepted, "n_accepted", torch.int32, (B,))
-    _same_device(kv_cache.device, k_pe_cache, block_table, cache_len, accepted, n_accepted)
-    _call("mla_cache_compact", kv_cache.device, stream,
-          (ctypes.byref(pages), _ptr(kv_cache), _ptr(k_pe_cache), _ptr(block_table), _ptr(cache_len), _ptr(accepted),
-           _ptr(n_accepted), B, accepted.shape[1]))
+    B = table[0]
+    if not cache_len.shape == n_accepted.shape == (B,):
+        raise ValueError("cache_len and n_accepted must be [B]")
+    pages = _pages(kv_cache, k_pe_cache, table[1], False)
+    index = _cuda(kv_cache)
+    _call("mla_cache_compact", index, stream,
+          (ctypes.byref(pages), _data(kv_cache, index), _data(k_pe_cache, index), _data(block_table, index),
+           _data(cache_len, index), _data(accepted, index), _data(n_accepted, index), B, nodes[1]))
 
 
 def mla_cache_copy_pages(kv_cache, k_pe_cache, src, dst, stream=None):
@@ -529,9 +546,10 @@ def mla_cache_copy_pages(kv_cache, k_pe_cache, src, dst, stream=None):
             v = v.tolist()
         lists.append(array.array("i", v))  # OverflowError for an index beyond 32 bits
     pages = _pages(kv_cache, k_pe_cache, 0, False)
-    _same_device(kv_cache.device, k_pe_cache)
-    _call("mla_cache_copy_pages", kv_cache.device, stream,
-          (ctypes.byref(pages), _ptr(kv_cache), _ptr(k_pe_cache), lists[0].buffer_info()[0], lists[1].buffer_info()[0], n))
+    index = _cuda(kv_cache)
+    _call("mla_cache_copy_pages", index, stream,
+          (ctypes.byref(pages), _data(kv_cache, index), _data(k_pe_cache, index), lists[0].buffer_info()[0],
+           lists[1].buffer_info()[0], n))
 
 
 def mla_device_status(stream=None) -> int:
