@@ -387,7 +387,7 @@ int mla_cache_append(const mla_rope_table* table, const void* kv_a, long long kv
  * lies outside [0, num_pages): that sequence's out rows are undefined (nothing
  * outside the caches is read); 402 cache_len < 0 or cache_len + n_nodes beyond
  * the table: that sequence's out rows are 0.
- * e4m3 weights are read as stored up to 256 rows (B N); more rows go through
+ * e4m3 weights are read as stored up to 768 rows (B N); more rows go through
  * bf16 copies in the workspace.
  * Workspace: mla_workspace_bytes(dims, MLA_ENTRY_TREE_DECODE, 0).
  * Errors: as for mla_decode; MLA_ERR_SHAPE also for bad pages or N, and for

@@ -294,49 +294,48 @@ gemm_m64_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
 // out[m, n] = bf16(sum of the stream-K partial tiles of tile (m / bm, n / 128)
 // over the CTAs c whose share meets it, by increasing c); `ctas` is the GEMM's
-// grid. One block per tile and 16 rows of it: thread 0 lists the tile's CTAs
-// (at most ctas / tiles + 2 of them, since every share holds at least
-// tiles * nkb / ctas units), then each thread adds two float4 columns.
+// grid, at most 256. One block per tile and 16 rows of it: each thread looks at
+// one CTA's share (two 64-bit divisions; one thread looking at them in turn
+// took 2 us), before the partial tiles are there, then adds two float4 columns.
 constexpr int kSumRows = 16;
-constexpr int kSumMaxParts = 64;
-__global__ void __launch_bounds__(256)
-sum_segments_kernel(const float* __restrict__ part, int M, int N, int K, int bm, int ctas,
-                    __nv_bfloat16* __restrict__ out, int* err) {
-  __shared__ int parts[kSumMaxParts];
-  __shared__ int nparts;
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads)
+sum_segments_kernel(const float* __restrict__ part, int M, int N, int K, int bm, int ctas, __nv_bfloat16* __restrict__ out) {
+  __shared__ int parts[kSumThreads];
+  __shared__ uint32_t found[kSumThreads / 32];
   griddep_launch();
-  griddep_wait();
   const int num_m = (M + bm - 1) / bm, nkb = K / 64;
   const int chunks = bm / kSumRows;
   const int t = blockIdx.x / chunks, r0 = (blockIdx.x % chunks) * kSumRows;
   const int mt = t % num_m, nt = t / num_m;
-  if (threadIdx.x == 0) {
+  const int c = static_cast<int>(threadIdx.x), warp = c >> 5;
+  bool meets = false;
+  if (c < ctas) {
     const int64_t units = static_cast<int64_t>(num_m) * (N / 128) * nkb;
     const int64_t lo = static_cast<int64_t>(t) * nkb, hi = lo + nkb;
-    int c = static_cast<int>(lo * ctas / units);  // the CTA whose share holds unit lo
-    while (c + 1 < ctas && stream_k_start(c + 1, units, ctas) <= lo) ++c;
-    int n = 0;
-    for (; c < ctas; ++c) {
-      const int64_t s0 = stream_k_start(c, units, ctas), s1 = stream_k_start(c + 1, units, ctas);
-      if (s0 >= hi) break;
-      if ((s1 < hi ? s1 : hi) <= (s0 > lo ? s0 : lo)) continue;  // an empty share
-      if (n == kSumMaxParts) {
-        atomicCAS(err, 0, kErrGeometry);
-        break;
-      }
-      parts[n++] = c;
-    }
-    nparts = n;
+    const int64_t s0 = stream_k_start(c, units, ctas), s1 = stream_k_start(c + 1, units, ctas);
+    meets = (s1 < hi ? s1 : hi) > (s0 > lo ? s0 : lo);
   }
+  const uint32_t mine = __ballot_sync(0xffffffffu, meets);
+  if ((c & 31) == 0) found[warp] = mine;
   __syncthreads();
-  const int n = nparts;
+  int n = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kSumThreads / 32; ++w) {
+    if (w < warp) before += __popc(found[w]);
+    n += __popc(found[w]);
+  }
+  if (meets) parts[before + __popc(mine & ((1u << (c & 31)) - 1u))] = c;
+  __syncthreads();
+  griddep_wait();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int q = threadIdx.x + 256 * h;  // float4 index in the 16 x 128 block
+    const int q = threadIdx.x + kSumThreads * h;  // float4 index in the 16 x 128 block
     const int r = r0 + q / 32, col = (q % 32) * 4;
     const int m = mt * bm + r;
     if (m >= M) continue;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const float4 v =
           *reinterpret_cast<const float4*>(part + (static_cast<size_t>(parts[i] + t) * bm + r) * 128 + col);

@@ -355,6 +355,7 @@ constexpr int kAbsChunkRows = 2048;
 // on the device; a different count only changes how full the waves are).
 constexpr int kSmsForSplit = 148;
 constexpr int kStreamKCtas = 256;  // upper bound on the stream-K grid (the SM count)
+static_assert(kStreamKCtas <= mla::kSumThreads, "a thread of the sum looks at one CTA");
 // K-split last wave of the prefill output projection (wo_split_plan): only
 // for K of at least kSplitMinTileKb 64-deep blocks (H >= 32; a shorter tile's
 // last wave ends before the partial sums would pay), each K range keeps at
@@ -367,6 +368,12 @@ constexpr int kSplitSlots = 74;
 // Up to this many rows the per-head GEMMs run on the few-row kernel (64- or
 // 128-row UMMA tiles, one CTA per item), beyond it on the CTA-pair GEMM.
 constexpr int kFewRows = 256;
+// Trees over e4m3 codes: read as stored up to this many rows (each 128 rows
+// convert them again), through bf16 copies (95 us, once) and the CTA-pair GEMM
+// beyond. 128 heads, all products: 256 rows 128 us against 231 with copies, 512
+// rows 218 against 238, 768 rows 322 against 338; 896 would be about 360.
+constexpr int kFewRowsE4m3 = 768;
+constexpr int64_t tree_few_rows(bool e4m3) { return e4m3 ? kFewRowsE4m3 : kFewRows; }
 // Cost model for MLA_PATH_AUTO: a tile group goes absorbed when its middle
 // row's causal prefix exceeds this many times the selection size. Measured
 // on B200 at T = 32768, H = 128, top-k 2048: the block-dense kernel costs
@@ -474,14 +481,14 @@ WsLayout ws_layout(const mla_dims& d, int entry, bool has_topk) {
     w.tree_start = take((static_cast<size_t>(d.B) + 2) * 8);
     w.tree_ml = take(size_t(2) * mla::kTreeMaxPairs * mla::kTreeRows * 8);
     w.tree_o = take(size_t(2) * mla::kTreeMaxPairs * mla::kTreeSlotFloats * 4);
-    if (rows <= kFewRows) {
+    if (rows <= tree_few_rows(fp8)) {
       const int bm = rows <= 64 ? 64 : 128;
       const size_t tiles = (rows + bm - 1) / bm * (kD / 128);
       w.wo_part = take((kStreamKCtas + tiles) * bm * 128 * 4);
     }
   }
   // Decoding reads bf16 copies of e4m3 weights; trees of few rows the codes.
-  const bool copies = entry == MLA_ENTRY_DECODE || (entry == MLA_ENTRY_TREE_DECODE && rows > kFewRows);
+  const bool copies = entry == MLA_ENTRY_DECODE || (entry == MLA_ENTRY_TREE_DECODE && rows > kFewRowsE4m3);
   const bool act8 = d.act == MLA_ACT_E4M3_DYNAMIC;
   if (act8) {
     if (attend || entry == MLA_ENTRY_KV_UPPROJECT) {
@@ -778,8 +785,8 @@ int launch_gemm_wo_m64(const DeviceState* ds, int M, int H, const void* attn, co
   const int blocks = ((M + bm - 1) / bm) * (N / GemmM64::BN) * (bm / mla::kSumRows);
   cudaError_t le = cudaSuccess;
   rc = timed_launch(4, st, [&] {
-    le = launch_kernel(mla::sum_segments_kernel, blocks, 256, 0, st, dependent, 1, part, M, N, K, bm, grid,
-                       static_cast<__nv_bfloat16*>(out), ds->err);
+    le = launch_kernel(mla::sum_segments_kernel, blocks, mla::kSumThreads, 0, st, dependent, 1, part, M, N, K, bm, grid,
+                       static_cast<__nv_bfloat16*>(out));
   });
   return le != cudaSuccess ? MLA_ERR_CUDA : rc;
 }
@@ -802,7 +809,7 @@ int launch_m64_w8(const DeviceState* ds, const CUtensorMap& ta, const CUtensorMa
 }
 
 // launch_gemm_absorb, launch_gemm_unabsorb and launch_gemm_wo_m64 of up to
-// kFewRows rows over e4m3 codes. o_lat comes with W_UV's scales multiplied in.
+// kFewRowsE4m3 rows over e4m3 codes. o_lat comes with W_UV's scales multiplied in.
 int launch_w8_absorb(const DeviceState* ds, int H, int rows, const void* q_rows, const void* codes, const float* scale,
                      void* qabs, cudaStream_t st) {
   CUtensorMap ta, tw;
@@ -848,8 +855,8 @@ int launch_w8_wo(const DeviceState* ds, int M, int H, const void* attn, const vo
   const int blocks = ((M + bm - 1) / bm) * (N / 128) * (bm / mla::kSumRows);
   cudaError_t le = cudaSuccess;
   rc = timed_launch(4, st, [&] {
-    le = launch_kernel(mla::sum_segments_kernel, blocks, 256, 0, st, true, 1, part, M, N, K, bm, grid,
-                       static_cast<__nv_bfloat16*>(out), ds->err);
+    le = launch_kernel(mla::sum_segments_kernel, blocks, mla::kSumThreads, 0, st, true, 1, part, M, N, K, bm, grid,
+                       static_cast<__nv_bfloat16*>(out));
   });
   return le != cudaSuccess ? MLA_ERR_CUDA : rc;
 }
@@ -1280,7 +1287,7 @@ int run_tree_decode(const DeviceState* ds, const mla_dims& d, const mla_pages& p
                     const int32_t* n_nodes, const int32_t* parents, const void* W_kvb, const float* W_kvb_scale,
                     const void* W_o, const float* W_o_scale, float scale, void* out, cudaStream_t st) {
   const int rows = d.B * d.T;
-  const bool few = rows <= kFewRows, e4m3 = d.wdtype == MLA_W_E4M3_BLOCK128;
+  const bool e4m3 = d.wdtype == MLA_W_E4M3_BLOCK128, few = rows <= tree_few_rows(e4m3);
   void* qabs = ws_at(ws, lay.qabs);
   void* olat = ws_at(ws, lay.olat);
   void* attn = ws_at(ws, lay.attn);

@@ -10,7 +10,12 @@ step's binade, 0.68 of that relative to the values (mantissas spread over the
 binade), 1.54e-3. The scores have a spread of about one (that of the recipe),
 so q_abs's rounding counts once. In quadrature: 3.4e-3 with five, 4.4e-3 with
 eight; 5e-3 relative L2 is asserted. The largest of up to 10^6 errors of that
-rms is within 8 of it: 4e-2 of the outputs' rms, plus the last half step.
+rms is within 8 of it: 4e-2 of the rms of their own output row, plus the last
+half step. The row's, not the tensor's: every rounding above is relative to
+values of the row itself, and rows differ. A node that sees n keys of unit
+variance averages them to about n^-1/2, so next to rows over 500 keys (0.045)
+stand rows over one (1.0) whose errors, 4.4e-3 rms, reach 5 x 4.4e-3 = 2.2e-2
+among 7168 values: with 64 such sequences 0.13 of the tensor's rms of 0.17.
 """
 import pytest
 import torch
@@ -113,8 +118,8 @@ def assert_near(got, want, rel=5e-3):
     err = (got - want)
     norm = want.norm()
     assert err.norm() <= rel * norm, float(err.norm() / norm)
-    rms = norm / want.numel() ** 0.5
-    assert (err.abs() <= 8 * rel * rms + HALF_STEP * want.abs()).all(), float(err.abs().max() / rms)
+    rms = want.square().mean(-1, keepdim=True).sqrt()
+    assert (err.abs() <= 8 * rel * rms + HALF_STEP * want.abs()).all(), float((err.abs() / rms.clamp_min(1e-30)).max())
 
 
 CASES = {
@@ -135,6 +140,9 @@ CASES = {
     "rows_above_256": dict(lens=[90 + 3 * b for b in range(70)], N=4, H=4),
     "e4m3_weights": dict(lens=[260, 33], N=4, H=4, fp8=True),
     "e4m3_rows_above_256": dict(lens=[50] * 70, N=4, H=2, fp8=True),
+    "e4m3_rows_512": dict(lens=[9 * b for b in range(64)], N=8, H=3, page=16, fp8=True),
+    "e4m3_rows_above_512": dict(lens=[40 + b for b in range(103)], N=5, H=2, fp8=True),
+    "e4m3_rows_above_768": dict(lens=[b % 40 for b in range(130)], N=6, H=2, page=32, fp8=True),
     "long": dict(lens=[9000, 20000, 33], N=2, H=8),
     "long_many_rows": dict(lens=[5000], N=40, H=64),
     "chain": dict(lens=[130, 61], N=7, H=4, tree=False),
