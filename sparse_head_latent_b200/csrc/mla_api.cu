@@ -373,7 +373,11 @@ constexpr int kFewRows = 256;
 // beyond. 128 heads, all products: 256 rows 128 us against 231 with copies, 512
 // rows 218 against 238, 768 rows 322 against 338; 896 would be about 360.
 constexpr int kFewRowsE4m3 = 768;
-constexpr int64_t tree_few_rows(bool e4m3) { return e4m3 ? kFewRowsE4m3 : kFewRows; }
+// Over bf16 weights: a step of 132, 192 and 256 rows took 157, 178 and 191 us on the
+// few-row kernels, launched as dependents, 158, 176 and 183 with W_o on the pair
+// GEMM, in plain launches.
+constexpr int kFewRowsTree = 192;
+constexpr int64_t tree_few_rows(bool e4m3) { return e4m3 ? kFewRowsE4m3 : kFewRowsTree; }
 // Cost model for MLA_PATH_AUTO: a tile group goes absorbed when its middle
 // row's causal prefix exceeds this many times the selection size. Measured
 // on B200 at T = 32768, H = 128, top-k 2048: the block-dense kernel costs

@@ -137,6 +137,7 @@ CASES = {
     "empty_and_tiny": dict(lens=[0, 0, 2, 1], N=4, H=6),
     "ragged_nodes": dict(lens=[100, 50, 700, 12, 90], N=8, H=16, nodes=[8, 0, 3, 1, 7]),
     "rows_above_64": dict(lens=[20 + b for b in range(100)], N=1, H=4, page=16),
+    "rows_above_192": dict(lens=[70 + 5 * b for b in range(49)], N=4, H=3, page=32),
     "rows_above_256": dict(lens=[90 + 3 * b for b in range(70)], N=4, H=4),
     "e4m3_weights": dict(lens=[260, 33], N=4, H=4, fp8=True),
     "e4m3_rows_above_256": dict(lens=[50] * 70, N=4, H=2, fp8=True),
