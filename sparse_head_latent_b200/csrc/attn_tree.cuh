@@ -40,9 +40,16 @@
 // which P.V(j - 1) covers). Those six travel through the ring, too: three groups
 // in front of a run's first block, which the softmax warps copy.
 //
-// Roles (352 threads per CTA): warps 0 and 10 producers, of keys and of values;
-// warp 1 of the leader issues the UMMAs; warps 2..9 softmax: four threads per row, one for each quarter of the block's
-// keys, agree on the running maximum through shared memory.
+// Roles (352 threads per CTA): warps 0 and 10 producers, of keys and of values
+// (warp 0 also walks the share and publishes its runs); warp 1 of the leader
+// issues the UMMAs; warps 2..9 softmax: four threads per row, one for each
+// quarter of the block's keys, agree on the running maximum through shared
+// memory.
+//
+// Measured: 8192 rows against 32768 keys 362 us, 1.61 PFLOP/s (tensor core);
+// 64 sequences of 128 rows and 30000 to 32768 keys 449 us, 5.2 TB/s of cache (L2
+// -> SM and HBM); 98 tiles of 4 to 63 blocks 105 us, half of it tensor core: a
+// run costs about three blocks before and after its products.
 #pragma once
 
 #include "gemm2.cuh"
@@ -499,7 +506,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         }
       }
     }
-    if (!ok) spin_ns(2000000);  // let issued loads land before the CTA can exit
   } else if (warp == 1) {
     if (rank == 0) {
       // ---------------- UMMA issuer, the whole warp (see umma_ss_pair_x4; each
@@ -822,6 +828,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
 
   tc_fence_before();
   __syncthreads();
+  // After a wait has run out in any warp, what others have asked for must land
+  // before the CTA can exit.
+  if (ab.raised()) spin_ns(2000000);
   cluster_sync();  // the leader's UMMAs read the other CTA's shared memory until here
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);

@@ -200,7 +200,6 @@ gemm_m64_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           }
         }
       }
-      if (!ok) spin_ns(2000000);  // let issued loads land before the CTA can exit
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -288,6 +287,9 @@ gemm_m64_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
   tc_fence_before();
   __syncthreads();
+  // After a wait has run out in any warp, what others have asked for must land
+  // before the CTA can exit.
+  if (ab.raised()) spin_ns(2000000);
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
 }

@@ -5,7 +5,12 @@
 // 128 heads are read, 268 MB written and read again, 89 us before the products
 // begin. Here each CTA's share of the codes goes from HBM to shared memory by
 // TMA and sixteen warps turn it into the bf16 operand there, so that a weight
-// costs one byte of HBM traffic. Scales (one per 128 x 128 block):
+// costs one byte of HBM traffic. W_o of 128 heads and 128 rows: 48 us, shared
+// memory busy for three quarters of it (codes and A written by TMA, codes read,
+// the operand written, both operands read by the tensor core: 80 KB for 8 KB of
+// codes). Tiles of 256 columns halve A's part, but leave two buffers of operand
+// for four: 1.5 us slower at 128 rows, 3.5 faster at 256.
+// Scales (one per 128 x 128 block):
 //   absorb  (q_nope . W_UK, K = 128): one scale per output tile, applied to the
 //           fp32 accumulator; the codes are exact in bf16
 //   unabsorb (o_lat . W_UV^T, K = 512): one scale per 128 of K, which the
@@ -150,7 +155,6 @@ gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
           }
         }
       }
-      if (!ok) spin_ns(2000000);  // let issued loads land before the CTA can exit
     }
   } else if (warp == 1) {
     // ---------------- UMMA issuer, the whole warp (see umma_ss_pair_x4)
@@ -305,6 +309,9 @@ gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 
   tc_fence_before();
   __syncthreads();
+  // After a wait has run out in any warp, what others have asked for must land
+  // before the CTA can exit.
+  if (ab.raised()) spin_ns(2000000);
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
 }

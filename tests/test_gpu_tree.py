@@ -359,6 +359,34 @@ def test_captured_graph_follows_its_inputs():
 # ------------------------------------------------------------------ upkeep
 
 
+def test_more_sequences_than_a_block_has_threads():
+    # several sequences per thread of the scan; some without nodes, some without a cache
+    B = 1111
+    p = Problem([(37 * b) % 150 if b % 9 else 0 for b in range(B)], 2, 2, page=16, nodes=[(b * 7) % 3 for b in range(B)])
+    out = p.run()
+    _no_device_error()
+    for b, n in enumerate(p.nodes):
+        assert not out[b, n:].any()
+    some = list(range(0, 30)) + list(range(340, 372)) + list(range(700, 712)) + [1109, 1110]
+    assert_near(out[some], p.expect(some)[some])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_no_sequence_has_a_node(fp8):
+    p = Problem([200, 0, 31], 3, 4, nodes=[0, 0, 0], fp8=fp8)
+    out = torch.full((3, 3, 7168), 7.0, dtype=torch.bfloat16, device="cuda")
+    p.run(out=out)
+    assert not out.any()
+    _no_device_error()
+
+
+def test_a_table_filled_to_its_last_position():
+    p = Problem([61, 30], 3, 4, page=64, spare=0)
+    assert p.table.shape[1] == 1
+    assert_near(p.run(), p.expect())
+    _no_device_error()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_two_graphs_share_a_workspace(fp8):
     # one step each of two models' batches, replayed in turn on one stream
