@@ -1662,16 +1662,23 @@ int mla_cache_compact(const mla_pages* pages, void* kv_cache, void* k_pe_cache, 
   p.err = ds->err;
   p.layers = pages->layers;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // Rows of a layer a thread holds: 2, 4 or 16, by the most that a sequence can
-  // accept; four layers a block unless the rows fill the registers.
-  const int per_block = width <= 4 * mla::kCompactRows ? 4 : 1;
-  const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>((pages->layers + per_block - 1) / per_block));
-  if (width <= 2 * mla::kCompactRows)
-    mla::cache_compact_kernel<2, 4><<<grid, mla::kCompactThreads, 0, st>>>(p);
-  else if (width <= 4 * mla::kCompactRows)
-    mla::cache_compact_kernel<4, 4><<<grid, mla::kCompactThreads, 0, st>>>(p);
+  auto launch = [&](auto kernel, int side, int layers) {
+    const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>((pages->layers + layers - 1) / layers));
+    kernel<<<grid, mla::kRowPieces * side, 0, st>>>(p);
+  };
+  // By the most rows that a sequence can accept: enough registers for them, and
+  // as many layers as leave two or more blocks on an SM. 64 sequences, 60 layers,
+  // this choice and the next best: up to 5 rows 6.5 us (two layers 7.2), up to
+  // 16 rows 15.7 (four layers 16.6, one 18), up to 32 rows 27.3 (two layers
+  // and eight rows side by side 28.4), 64 rows each 97.7 (two layers 99.6).
+  if (width <= 8)
+    launch(mla::cache_compact_kernel<4, 2, 4>, 4, 4);
+  else if (width <= 16)
+    launch(mla::cache_compact_kernel<4, 4, 2>, 4, 2);
+  else if (width <= 32)
+    launch(mla::cache_compact_kernel<4, 8, 1>, 4, 1);
   else
-    mla::cache_compact_kernel<MLA_MAX_TREE / mla::kCompactRows, 1><<<grid, mla::kCompactThreads, 0, st>>>(p);
+    launch(mla::cache_compact_kernel<8, 8, 1>, 8, 1);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

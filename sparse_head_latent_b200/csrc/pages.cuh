@@ -27,67 +27,61 @@ struct CompactParams {
   int* err;
 };
 
-constexpr int kCompactRows = 4;                           // rows that a block moves side by side
-constexpr int kCompactThreads = kRowPieces * kCompactRows;
 
 // Block (b, LAYERS layers): row cache_len + accepted[i] of the sequence to row
 // cache_len + i, for i < counts[b]. Sources and destinations overlap (a
 // destination can be a later source), so the block reads all its rows into
 // registers, waits for all its threads, and only then writes; no other block
-// touches this sequence's rows of these layers. PER = rows of a layer a thread
-// holds. The rows are found through two loads in a row (length, count and node,
-// then page), once for all the block's layers. 64 sequences, 60 layers, up to 16
-// rows each, 71 MB moved: 16.3 us with four layers a block, 17.5 with one.
-template <int PER, int LAYERS>
-__global__ void __launch_bounds__(kCompactThreads)
+// touches this sequence's rows of these layers. SIDE rows are moved side by side,
+// and a thread holds PER of a layer. The rows are found one per thread, through
+// two loads in a row (length, count and node, then page), and passed on in shared
+// memory. 64 sequences, 60 layers, up to 16 rows each, 71 MB moved: 15.7 us; up
+// to 32 rows, 141 MB: 27.3. With every thread looking for its rows itself 20.5
+// and 108.
+template <int SIDE, int PER, int LAYERS>
+__global__ void __launch_bounds__(kRowPieces * SIDE)
 cache_compact_kernel(const CompactParams p) {
-  const int b = blockIdx.x;
+  __shared__ int from[SIDE * PER], to[SIDE * PER];
+  const int b = blockIdx.x, i = static_cast<int>(threadIdx.x);
+  const int node = i < p.width ? __ldg(p.accepted + static_cast<int64_t>(b) * p.width + i) : -1;
   const int count = min(__ldg(p.counts + b), p.width);
   const int64_t len = __ldg(p.cache_len + b);
-  const int c = static_cast<int>(threadIdx.x) % kRowPieces, r0 = static_cast<int>(threadIdx.x) / kRowPieces;
-  int node[PER];  // asked for together with the count
-#pragma unroll
-  for (int k = 0; k < PER; ++k)
-    node[k] = r0 + k * kCompactRows < p.width ? __ldg(p.accepted + static_cast<int64_t>(b) * p.width + r0 + k * kCompactRows) : -1;
   if (count <= 0) return;
+  if (i < count) {
+    // cache row of position t, or -1 when it lies outside the table or the cache
+    auto place = [&](int64_t t) -> int {
+      const int64_t at = t >> p.page_shift;
+      if (t < 0 || at >= p.table_width) return -1;
+      const int page = __ldg(p.table + static_cast<int64_t>(b) * p.table_width + at);
+      if (page < 0 || page >= p.num_pages) return -1;
+      return (page << p.page_shift) + static_cast<int>(t & ((1 << p.page_shift) - 1));
+    };
+    const int f = node < 0 ? -1 : place(len + node), t = place(len + i);
+    if (f < 0 || t < 0) atomicCAS(p.err, 0, kErrPage);
+    from[i] = f;
+    to[i] = f < 0 || f == t ? -1 : t;  // f == t: already there
+  }
+  __syncthreads();
   const int64_t rows = static_cast<int64_t>(p.num_pages) << p.page_shift;
   const int layer0 = static_cast<int>(blockIdx.y) * LAYERS;
-  // cache row of position t, or -1 when it lies outside the table or the cache
-  auto place = [&](int64_t t) -> int64_t {
-    const int64_t at = t >> p.page_shift;
-    if (t < 0 || at >= p.table_width) return -1;
-    const int page = __ldg(p.table + static_cast<int64_t>(b) * p.table_width + at);
-    if (page < 0 || page >= p.num_pages) return -1;
-    return (static_cast<int64_t>(page) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
-  };
+  const int c = i % kRowPieces, r0 = i / kRowPieces;
   uint4 v[PER][LAYERS];
-  int64_t to[PER];
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
-    const int i = r0 + k * kCompactRows;
-    to[k] = -1;
-    if (i < count) {
-      const int64_t from = node[k] < 0 ? -1 : place(len + node[k]);
-      to[k] = place(len + i);
-      if (from < 0 || to[k] < 0) {
-        if (c == 0) atomicCAS(p.err, 0, kErrPage);
-        to[k] = -1;
-      } else if (from == to[k]) {
-        to[k] = -1;  // already there
-      } else {
+    const int r = r0 + k * SIDE;
+    if (r >= count || to[r] < 0) continue;
 #pragma unroll
-        for (int l = 0; l < LAYERS; ++l)
-          if (layer0 + l < p.layers) v[k][l] = *cache_piece(p.kv, p.pe, (layer0 + l) * rows + from, c);
-      }
-    }
+    for (int l = 0; l < LAYERS; ++l)
+      if (layer0 + l < p.layers) v[k][l] = *cache_piece(p.kv, p.pe, (layer0 + l) * rows + from[r], c);
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
-    if (to[k] < 0) continue;
+    const int r = r0 + k * SIDE;
+    if (r >= count || to[r] < 0) continue;
 #pragma unroll
     for (int l = 0; l < LAYERS; ++l)
-      if (layer0 + l < p.layers) *cache_piece(p.kv, p.pe, (layer0 + l) * rows + to[k], c) = v[k][l];
+      if (layer0 + l < p.layers) *cache_piece(p.kv, p.pe, (layer0 + l) * rows + to[r], c) = v[k][l];
   }
 }
 
