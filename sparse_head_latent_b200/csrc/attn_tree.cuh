@@ -837,15 +837,21 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
 }
 
 // Joins the tiles that several pairs shared, and zeroes the rows of nodes that
-// are not there. Thread: one row of a tile, 16 of its values; with M the
+// are not there. Thread: one row of a tile, VALUES of its values; with M the
 // largest of the parts' maxima, o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p
 // over the pairs p whose shares meet the tile, in their order. The pairs are
 // found side by side, one per thread: one after the other, with their 64-bit
-// divisions, took 40 us for a tile of eight parts.
+// divisions, took 40 us for a tile of eight parts. With 16 values a thread a
+// tile is 16 blocks; where the tiles give fewer than two blocks per SM so, four
+// values and the parts eight at a time. One sequence of 32768, one token of 128
+// heads (one tile of 74 parts): a step of 99 us, 148 with 16 values. 16 tiles: 98
+// and 97. 98 tiles: fewer values a thread (eight) cost 4 us.
 constexpr int kTreeJoinThreads = 256;
-constexpr int kTreeJoinBlocks = kTreeRows * 32 / kTreeJoinThreads;  // per tile
+template <int VALUES>
+constexpr int kTreeJoinBlocks = kTreeRows * (512 / VALUES) / kTreeJoinThreads;  // per tile
 static_assert(kTreeMaxPairs <= 96, "three warps look for the parts");
 
+template <int VALUES>
 __global__ void __launch_bounds__(kTreeJoinThreads)
 tree_combine_kernel(const TreeParams p, int pairs) {
   __shared__ int slots[96];
@@ -853,9 +859,10 @@ tree_combine_kernel(const TreeParams p, int pairs) {
   griddep_launch();
   griddep_wait();
   const int all_tiles = (p.N * p.H + kTreeRows - 1) / kTreeRows;
-  const int at = static_cast<int>(blockIdx.x) / kTreeJoinBlocks, b = at / all_tiles, tile = at % all_tiles;
-  const int item = static_cast<int>(blockIdx.x) % kTreeJoinBlocks * kTreeJoinThreads + static_cast<int>(threadIdx.x);
-  const int tr = item & 127, v0 = (item >> 7) * 16;
+  constexpr int BLOCKS = kTreeJoinBlocks<VALUES>, QUADS = VALUES / 4, BATCH = 32 / VALUES;
+  const int at = static_cast<int>(blockIdx.x) / BLOCKS, b = at / all_tiles, tile = at % all_tiles;
+  const int item = static_cast<int>(blockIdx.x) % BLOCKS * kTreeJoinThreads + static_cast<int>(threadIdx.x);
+  const int tr = item & 127, v0 = (item >> 7) * VALUES;
   const int r = tile * kTreeRows + tr;
   // Asked for before the lengths are looked at.
   const int64_t units = p.ustart[p.B], extra = p.ustart[p.B + 1], first = p.ustart[b];
@@ -884,45 +891,61 @@ tree_combine_kernel(const TreeParams p, int pairs) {
     slots[(c >= 64 ? n0 + n1 : c >= 32 ? n0 : 0) + __popc(static_cast<uint32_t>(found[c >> 5]) & ((1u << (c & 31)) - 1))] = slot;
   __syncthreads();
   if (r >= p.N * p.H) return;
-  uint4* dst = reinterpret_cast<uint4*>(p.olat + (static_cast<int64_t>(b) * p.N * p.H + r) * 512 + v0);
+  uint2* dst = reinterpret_cast<uint2*>(p.olat + (static_cast<int64_t>(b) * p.N * p.H + r) * 512 + v0);
   if (r >= nodes * p.H) {
-    dst[0] = dst[1] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int k = 0; k < QUADS; ++k) dst[k] = make_uint2(0u, 0u);
     return;
   }
   if (n == 0) return;  // one pair's alone
   float M = -INFINITY;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < n; ++i) M = fmaxf(M, p.part_ml[slots[i] * kTreeRows + tr].x);
-  float acc[16], sum = 0.f;
+  float4 acc[QUADS];
+  float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll 2
-  for (int i = 0; i < n; ++i) {
-    const float2 ml = p.part_ml[slots[i] * kTreeRows + tr];
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(slots[i]) * kTreeSlotFloats) +
-                        v0 / 4 * kTreeRows + tr;
-    float4 v[4];
+  for (int k = 0; k < QUADS; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += BATCH) {
+    float2 ml[BATCH];
+    float4 v[BATCH][QUADS];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = src[k * kTreeRows];
-    if (ml.y == 0.f) continue;  // saw none of its keys
-    const float w = ex2_approx(ml.x - M);
-    sum = fmaf(w, ml.y, sum);
+    for (int u = 0; u < BATCH; ++u) {
+      ml[u].y = 0.f;
+      if (i0 + u >= n) continue;
+      const int s = slots[i0 + u];
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(s) * kTreeSlotFloats) +
+                          v0 / 4 * kTreeRows + tr;
+      ml[u] = p.part_ml[s * kTreeRows + tr];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      acc[4 * k] = fmaf(w, v[k].x, acc[4 * k]);
-      acc[4 * k + 1] = fmaf(w, v[k].y, acc[4 * k + 1]);
-      acc[4 * k + 2] = fmaf(w, v[k].z, acc[4 * k + 2]);
-      acc[4 * k + 3] = fmaf(w, v[k].w, acc[4 * k + 3]);
+      for (int k = 0; k < QUADS; ++k) v[u][k] = src[k * kTreeRows];
+    }
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      if (ml[u].y == 0.f) continue;  // no part, or it saw none of its keys
+      const float w = ex2_approx(ml[u].x - M);
+      sum = fmaf(w, ml[u].y, sum);
+#pragma unroll
+      for (int k = 0; k < QUADS; ++k)
+        acc[k] = make_float4(fmaf(w, v[u][k].x, acc[k].x), fmaf(w, v[u][k].y, acc[k].y), fmaf(w, v[u][k].z, acc[k].z),
+                             fmaf(w, v[u][k].w, acc[k].w));
     }
   }
   float inv = sum != 0.f ? 1.f / sum : 0.f;
   if (p.v_scale != nullptr) inv *= __ldg(p.v_scale + (2 * (r % p.H) + 1) * 4 + (v0 >> 7));
+  uint32_t o[2 * QUADS];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    dst[i] = make_uint4(pack_bf16x2(acc[8 * i] * inv, acc[8 * i + 1] * inv),
-                        pack_bf16x2(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv),
-                        pack_bf16x2(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv),
-                        pack_bf16x2(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
+  for (int k = 0; k < QUADS; ++k) {
+    o[2 * k] = pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
+    o[2 * k + 1] = pack_bf16x2(acc[k].z * inv, acc[k].w * inv);
+  }
+  if constexpr (QUADS == 1) {
+    *dst = make_uint2(o[0], o[1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < QUADS / 2; ++k)
+      reinterpret_cast<uint4*>(dst)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+  }
 }
 
 }  // namespace mla

@@ -1277,10 +1277,12 @@ int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pa
   });
   if (le != cudaSuccess) return MLA_ERR_CUDA;
   if (rc != MLA_OK) return rc;
-  const int64_t join = static_cast<int64_t>(d.B) * ((d.T * d.H + mla::kTreeRows - 1) / mla::kTreeRows) * mla::kTreeJoinBlocks;
+  const int64_t tiles = static_cast<int64_t>(d.B) * ((d.T * d.H + mla::kTreeRows - 1) / mla::kTreeRows);
+  const bool many = tiles * mla::kTreeJoinBlocks<16> >= 2 * ds->sms;
+  const int64_t join = tiles * (many ? mla::kTreeJoinBlocks<16> : mla::kTreeJoinBlocks<4>);
   rc = timed_launch(7, st, [&] {
-    le = launch_kernel(mla::tree_combine_kernel, static_cast<unsigned>(join), mla::kTreeJoinThreads, 0, st, dependent, 1, p,
-                       ds->pairs_tree);
+    le = launch_kernel(many ? mla::tree_combine_kernel<16> : mla::tree_combine_kernel<4>, static_cast<unsigned>(join),
+                       mla::kTreeJoinThreads, 0, st, dependent, 1, p, ds->pairs_tree);
   });
   return le != cudaSuccess ? MLA_ERR_CUDA : rc;
 }

@@ -436,7 +436,8 @@ def _caches(layers, pages, page, seed=0):
     return [torch.randn(*shape, n, generator=g, device="cuda").to(torch.bfloat16) for n in (512, 64)]
 
 
-@pytest.mark.parametrize("layers,page,width", [(None, 16, 3), (1, 16, 8), (3, 64, 9), (2, 32, 16), (2, 16, 64)])
+@pytest.mark.parametrize("layers,page,width", [(None, 16, 3), (1, 16, 8), (3, 64, 9), (2, 32, 16), (2, 16, 64),
+                                               (5, 16, 1), (4, 32, 17), (3, 16, 32), (2, 64, 33)])
 def test_compact_moves_the_accepted_rows(layers, page, width):
     B, cols = 5, 12
     kv, pe = _caches(layers, B * cols + 2, page)
