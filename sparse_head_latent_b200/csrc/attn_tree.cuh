@@ -841,27 +841,37 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
 // largest of the parts' maxima, o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p
 // over the pairs p whose shares meet the tile, in their order. The pairs are
 // found side by side, one per thread: one after the other, with their 64-bit
-// divisions, took 40 us for a tile of eight parts. With 16 values a thread a
-// tile is 16 blocks; where the tiles give fewer than two blocks per SM so, four
-// values and the parts eight at a time. One sequence of 32768, one token of 128
-// heads (one tile of 74 parts): a step of 99 us, 148 with 16 values. 16 tiles: 98
-// and 97. 98 tiles: fewer values a thread (eight) cost 4 us.
-constexpr int kTreeJoinThreads = 256;
-template <int VALUES>
-constexpr int kTreeJoinBlocks = kTreeRows * (512 / VALUES) / kTreeJoinThreads;  // per tile
+// divisions, took 40 us for a tile of eight parts. Three shapes, by the tiles:
+//   many   16 values, two parts on their way, 16 blocks a tile
+//   some   4 values, eight parts, 64 blocks: where many would give fewer than two
+//          blocks per SM. 8 tiles of 8 parts: a step of 93 us, 101 with 16 values;
+//          16 tiles 97 and 97; 98 tiles with 8 values 4 us slower than with 16
+//   few    4 values, and four teams of a block that take every fourth part, 128
+//          blocks: where all of them are resident at once. One tile of 74 parts
+//          (one sequence of 32768, one token of 128 heads) 87 us, 99 as some, 148
+//          as many; 2 tiles 84 and 90, 3 tiles 92 and 93, 6 tiles 102 and 100
+template <int VALUES, int TEAMS>
+struct TreeJoin {
+  static constexpr int TEAM = TEAMS > 1 ? kTreeRows : 256;              // threads
+  static constexpr int THREADS = TEAM * TEAMS;
+  static constexpr int BLOCKS = kTreeRows * (512 / VALUES) / TEAM;      // per tile
+  static constexpr int QUADS = VALUES / 4, BATCH = TEAMS > 1 ? 4 : 32 / VALUES;  // parts on their way at once
+};
 static_assert(kTreeMaxPairs <= 96, "three warps look for the parts");
 
-template <int VALUES>
-__global__ void __launch_bounds__(kTreeJoinThreads)
+template <int VALUES, int TEAMS>
+__global__ void __launch_bounds__(TreeJoin<VALUES, TEAMS>::THREADS, TEAMS > 1 ? 2 : 1)
 tree_combine_kernel(const TreeParams p, int pairs) {
+  using J = TreeJoin<VALUES, TEAMS>;
+  constexpr int QUADS = J::QUADS, BATCH = J::BATCH;
   __shared__ int slots[96];
   __shared__ int found[3];
   griddep_launch();
   griddep_wait();
   const int all_tiles = (p.N * p.H + kTreeRows - 1) / kTreeRows;
-  constexpr int BLOCKS = kTreeJoinBlocks<VALUES>, QUADS = VALUES / 4, BATCH = 32 / VALUES;
-  const int at = static_cast<int>(blockIdx.x) / BLOCKS, b = at / all_tiles, tile = at % all_tiles;
-  const int item = static_cast<int>(blockIdx.x) % BLOCKS * kTreeJoinThreads + static_cast<int>(threadIdx.x);
+  const int at = static_cast<int>(blockIdx.x) / J::BLOCKS, b = at / all_tiles, tile = at % all_tiles;
+  const int team = static_cast<int>(threadIdx.x) / J::TEAM;
+  const int item = static_cast<int>(blockIdx.x) % J::BLOCKS * J::TEAM + static_cast<int>(threadIdx.x) % J::TEAM;
   const int tr = item & 127, v0 = (item >> 7) * VALUES;
   const int r = tile * kTreeRows + tr;
   // Asked for before the lengths are looked at.
@@ -890,30 +900,29 @@ tree_combine_kernel(const TreeParams p, int pairs) {
   if (slot >= 0)
     slots[(c >= 64 ? n0 + n1 : c >= 32 ? n0 : 0) + __popc(static_cast<uint32_t>(found[c >> 5]) & ((1u << (c & 31)) - 1))] = slot;
   __syncthreads();
-  if (r >= p.N * p.H) return;
   uint2* dst = reinterpret_cast<uint2*>(p.olat + (static_cast<int64_t>(b) * p.N * p.H + r) * 512 + v0);
-  if (r >= nodes * p.H) {
+  const bool live = r < nodes * p.H;
+  if (!live && r < p.N * p.H && team == 0) {
 #pragma unroll
     for (int k = 0; k < QUADS; ++k) dst[k] = make_uint2(0u, 0u);
-    return;
   }
   if (n == 0) return;  // one pair's alone
   float M = -INFINITY;
 #pragma unroll 8
-  for (int i = 0; i < n; ++i) M = fmaxf(M, p.part_ml[slots[i] * kTreeRows + tr].x);
+  for (int i = team; live && i < n; i += TEAMS) M = fmaxf(M, p.part_ml[slots[i] * kTreeRows + tr].x);
   float4 acc[QUADS];
   float sum = 0.f;
 #pragma unroll
   for (int k = 0; k < QUADS; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += BATCH) {
+  for (int i0 = team; live && i0 < n; i0 += BATCH * TEAMS) {
     float2 ml[BATCH];
     float4 v[BATCH][QUADS];
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
       ml[u].y = 0.f;
-      if (i0 + u >= n) continue;
-      const int s = slots[i0 + u];
+      if (i0 + u * TEAMS >= n) continue;
+      const int s = slots[i0 + u * TEAMS];
       const float4* src = reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(s) * kTreeSlotFloats) +
                           v0 / 4 * kTreeRows + tr;
       ml[u] = p.part_ml[s * kTreeRows + tr];
@@ -931,6 +940,37 @@ tree_combine_kernel(const TreeParams p, int pairs) {
                              fmaf(w, v[u][k].w, acc[k].w));
     }
   }
+  if constexpr (TEAMS > 1) {
+    __shared__ float joined[TEAMS - 1][2 + VALUES][kTreeRows];
+    if (team > 0) {
+      float(*j)[kTreeRows] = joined[team - 1];
+      j[0][tr] = M;
+      j[1][tr] = sum;
+#pragma unroll
+      for (int k = 0; k < QUADS; ++k)
+        j[4 * k + 2][tr] = acc[k].x, j[4 * k + 3][tr] = acc[k].y, j[4 * k + 4][tr] = acc[k].z, j[4 * k + 5][tr] = acc[k].w;
+    }
+    __syncthreads();
+    if (team > 0) return;
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < TEAMS - 1; ++i) top = fmaxf(top, joined[i][0][tr]);
+    const float base = top == -INFINITY ? 0.f : top, own = ex2_approx(M - base);
+    sum *= own;
+#pragma unroll
+    for (int k = 0; k < QUADS; ++k) acc[k] = make_float4(acc[k].x * own, acc[k].y * own, acc[k].z * own, acc[k].w * own);
+#pragma unroll
+    for (int i = 0; i < TEAMS - 1; ++i) {
+      const float(*j)[kTreeRows] = joined[i];
+      const float w = ex2_approx(j[0][tr] - base);
+      sum = fmaf(w, j[1][tr], sum);
+#pragma unroll
+      for (int k = 0; k < QUADS; ++k)
+        acc[k] = make_float4(fmaf(w, j[4 * k + 2][tr], acc[k].x), fmaf(w, j[4 * k + 3][tr], acc[k].y),
+                             fmaf(w, j[4 * k + 4][tr], acc[k].z), fmaf(w, j[4 * k + 5][tr], acc[k].w));
+    }
+  }
+  if (!live) return;
   float inv = sum != 0.f ? 1.f / sum : 0.f;
   if (p.v_scale != nullptr) inv *= __ldg(p.v_scale + (2 * (r % p.H) + 1) * 4 + (v0 >> 7));
   uint32_t o[2 * QUADS];

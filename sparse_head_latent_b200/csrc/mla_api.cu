@@ -1278,11 +1278,19 @@ int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pa
   if (le != cudaSuccess) return MLA_ERR_CUDA;
   if (rc != MLA_OK) return rc;
   const int64_t tiles = static_cast<int64_t>(d.B) * ((d.T * d.H + mla::kTreeRows - 1) / mla::kTreeRows);
-  const bool many = tiles * mla::kTreeJoinBlocks<16> >= 2 * ds->sms;
-  const int64_t join = tiles * (many ? mla::kTreeJoinBlocks<16> : mla::kTreeJoinBlocks<4>);
+  using Many = mla::TreeJoin<16, 1>;
+  using Some = mla::TreeJoin<4, 1>;
+  using Few = mla::TreeJoin<4, 4>;
   rc = timed_launch(7, st, [&] {
-    le = launch_kernel(many ? mla::tree_combine_kernel<16> : mla::tree_combine_kernel<4>, static_cast<unsigned>(join),
-                       mla::kTreeJoinThreads, 0, st, dependent, 1, p, ds->pairs_tree);
+    auto join = [&](auto kernel, int64_t blocks, int threads) {
+      le = launch_kernel(kernel, static_cast<unsigned>(tiles * blocks), threads, 0, st, dependent, 1, p, ds->pairs_tree);
+    };
+    if (tiles * Few::BLOCKS <= 2 * ds->sms)
+      join(mla::tree_combine_kernel<4, 4>, Few::BLOCKS, Few::THREADS);
+    else if (tiles * Many::BLOCKS < 2 * ds->sms)
+      join(mla::tree_combine_kernel<4, 1>, Some::BLOCKS, Some::THREADS);
+    else
+      join(mla::tree_combine_kernel<16, 1>, Many::BLOCKS, Many::THREADS);
   });
   return le != cudaSuccess ? MLA_ERR_CUDA : rc;
 }

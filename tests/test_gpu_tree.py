@@ -145,6 +145,11 @@ CASES = {
     "e4m3_rows_above_512": dict(lens=[40 + b for b in range(103)], N=5, H=2, fp8=True),
     "e4m3_rows_above_768": dict(lens=[b % 40 for b in range(130)], N=6, H=2, page=32, fp8=True),
     "long": dict(lens=[9000, 20000, 33], N=2, H=8),
+    "one_long": dict(lens=[20000], N=1, H=128, tree=False),
+    "one_long_few_rows": dict(lens=[9890], N=5, H=8, page=16),
+    "two_long": dict(lens=[9000, 7000], N=3, H=16, page=32, nodes=[3, 1]),
+    "two_long_e4m3": dict(lens=[3000, 7000], N=3, H=16, page=32, fp8=True),
+    "eight_long": dict(lens=[2000 + 700 * b for b in range(8)], N=2, H=40),
     "long_many_rows": dict(lens=[5000], N=40, H=64),
     "chain": dict(lens=[130, 61], N=7, H=4, tree=False),
 }
