@@ -157,10 +157,27 @@ def mla_workspace_bytes(dims: MlaDims, entry: int, has_topk: bool) -> int:
     return int(load_library().mla_workspace_bytes(ctypes.byref(dims), int(entry), 1 if has_topk else 0))
 
 
-def _workspace(dims, entry, has_topk, workspace, device):
+def _new(shape, dtype, device, stream, returned=True):
+    """An uninitialised tensor for a call on `stream` (None: the current one). The caching allocator hands out a block
+    again as soon as it is freed, ordered with the block's own stream only, so the tensor comes from the pool of the
+    stream that writes it: from the current stream's, it could still be in use there. `returned`: the caller gets it,
+    on the current stream, whose work must then be done before the block is handed out again."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(current)
+    return t
+
+
+def _workspace(dims, entry, has_topk, workspace, device, stream):
     need = mla_workspace_bytes(dims, entry, has_topk)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        workspace = _new(max(need, 1), torch.uint8, device, stream, returned=False)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -171,8 +188,8 @@ def mla_kv_upproject(kv_latent, W_kvb, W_kvb_scale=None, kvh_out=None, workspace
     H = W_kvb.shape[0] // (D_NOPE + D_V)
     dims = make_dims(1, rows, H, 0, _wtype(W_kvb), act=act)
     if kvh_out is None:
-        kvh_out = torch.empty(rows, H * (D_NOPE + D_V), dtype=torch.bfloat16, device=kv_latent.device)
-    ws, nbytes = _workspace(dims, MLA_ENTRY_KV_UPPROJECT, False, workspace, kv_latent.device)
+        kvh_out = _new((rows, H * (D_NOPE + D_V)), torch.bfloat16, kv_latent.device, stream)
+    ws, nbytes = _workspace(dims, MLA_ENTRY_KV_UPPROJECT, False, workspace, kv_latent.device, stream)
     lib = load_library()
     _check("mla_kv_upproject", lib.mla_kv_upproject(ctypes.byref(dims), _ptr(kv_latent), _ptr(W_kvb),
                                                     _ptr(W_kvb_scale), _ptr(kvh_out), _ptr(ws), nbytes,
@@ -189,8 +206,8 @@ def mla_attend(q, kv_latent, k_pe, W_kvb, W_kvb_scale=None, topk_idx=None, scale
     if topk_idx is not None and topk_idx.dtype != torch.int32:
         raise ValueError("topk_idx must be int32")
     if attn_out is None:
-        attn_out = torch.empty(B, T, H, D_V, dtype=torch.bfloat16, device=q.device)
-    ws, nbytes = _workspace(dims, MLA_ENTRY_ATTEND, topk_idx is not None, workspace, q.device)
+        attn_out = _new((B, T, H, D_V), torch.bfloat16, q.device, stream)
+    ws, nbytes = _workspace(dims, MLA_ENTRY_ATTEND, topk_idx is not None, workspace, q.device, stream)
     lib = load_library()
     _check("mla_attend", lib.mla_attend(ctypes.byref(dims), _ptr(q), _ptr(kv_latent), _ptr(k_pe), _ptr(W_kvb),
                                         _ptr(W_kvb_scale), _ptr(topk_idx), float(scale), _ptr(attn_out),
@@ -212,7 +229,7 @@ def mla_attend_static(q, kv_latent, k_pe, W_kvb, W_kvb_scale=None, topk_idx=None
     if topk_idx is not None and topk_idx.dtype != torch.int32:
         raise ValueError("topk_idx must be int32")
     if attn_out is None:
-        attn_out = torch.empty(B, T, H, D_V, dtype=torch.bfloat16, device=q.device)
+        attn_out = _new((B, T, H, D_V), torch.bfloat16, q.device, stream)
     _check("mla_attend_static", load_library().mla_attend_static(
         ctypes.byref(dims), _ptr(q), _ptr(kv_latent), _ptr(k_pe), _ptr(W_kvb), _ptr(W_kvb_scale), _ptr(topk_idx),
         float(scale), _ptr(attn_out), _stream(stream)))
@@ -225,8 +242,8 @@ def mla_out_project(attn, W_o, W_o_scale=None, out=None, workspace=None, stream=
     rows = attn.numel() // (H * D_V)
     dims = make_dims(1, rows, H, 0, _wtype(W_o), act=act)
     if out is None:
-        out = torch.empty(rows, D_MODEL, dtype=torch.bfloat16, device=attn.device)
-    ws, nbytes = _workspace(dims, MLA_ENTRY_OUT_PROJECT, False, workspace, attn.device)
+        out = _new((rows, D_MODEL), torch.bfloat16, attn.device, stream)
+    ws, nbytes = _workspace(dims, MLA_ENTRY_OUT_PROJECT, False, workspace, attn.device, stream)
     lib = load_library()
     _check("mla_out_project", lib.mla_out_project(ctypes.byref(dims), _ptr(attn), _ptr(W_o), _ptr(W_o_scale),
                                                   _ptr(out), _ptr(ws), nbytes, _stream(stream)))
@@ -245,8 +262,8 @@ def mla_prefill(q, kv_latent, k_pe, W_kvb, W_o, W_kvb_scale=None, W_o_scale=None
         raise ValueError("topk_idx must be int32")
     dims = make_dims(B, T, H, topk, fp8, path, act)
     if out is None:
-        out = torch.empty(B, T, D_MODEL, dtype=torch.bfloat16, device=q.device)
-    ws, nbytes = _workspace(dims, MLA_ENTRY_PREFILL, topk_idx is not None, workspace, q.device)
+        out = _new((B, T, D_MODEL), torch.bfloat16, q.device, stream)
+    ws, nbytes = _workspace(dims, MLA_ENTRY_PREFILL, topk_idx is not None, workspace, q.device, stream)
     lib = load_library()
     _check("mla_prefill", lib.mla_prefill(ctypes.byref(dims), _ptr(q), _ptr(kv_latent), _ptr(k_pe), _ptr(W_kvb),
                                           _ptr(W_kvb_scale), _ptr(W_o), _ptr(W_o_scale), _ptr(topk_idx),
@@ -268,8 +285,8 @@ def mla_decode(q, kv_latent, k_pe, W_kvb, W_o, W_kvb_scale=None, W_o_scale=None,
         raise ValueError("topk_idx must be int32")
     dims = make_dims(B, T, H, topk, fp8)
     if out is None:
-        out = torch.empty(B, D_MODEL, dtype=torch.bfloat16, device=q.device)
-    ws, nbytes = _workspace(dims, MLA_ENTRY_DECODE, topk_idx is not None, workspace, q.device)
+        out = _new((B, D_MODEL), torch.bfloat16, q.device, stream)
+    ws, nbytes = _workspace(dims, MLA_ENTRY_DECODE, topk_idx is not None, workspace, q.device, stream)
     lib = load_library()
     _check("mla_decode", lib.mla_decode(ctypes.byref(dims), _ptr(q), _ptr(kv_latent), _ptr(k_pe), _ptr(W_kvb),
                                         _ptr(W_kvb_scale), _ptr(W_o), _ptr(W_o_scale), _ptr(topk_idx), float(scale),
@@ -284,9 +301,9 @@ def mla_quantize_act(x, codes=None, scales=None, stream=None):
         raise ValueError("x must be bf16")
     rows, cols = x.reshape(-1, x.shape[-1]).shape
     if codes is None:
-        codes = torch.empty(rows, cols, dtype=torch.uint8, device=x.device)
+        codes = _new((rows, cols), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty(cols // 128 if cols % 128 == 0 else 0, rows, dtype=torch.float32, device=x.device)
+        scales = _new((cols // 128 if cols % 128 == 0 else 0, rows), torch.float32, x.device, stream)
     _check("mla_quantize_act", load_library().mla_quantize_act(_ptr(x), rows, cols, _ptr(codes), _ptr(scales),
                                                                _stream(stream)))
     return codes, scales
@@ -328,15 +345,12 @@ def _data(t, index, strided=False):
     return t.data_ptr()
 
 
-def _call(name, index, stream, args, used=()):
-    """Runs an entry point on CUDA device `index`, on `stream` or that device's current stream. `used`: tensors
-    allocated here, which the caching allocator must not hand out again before `stream` is done with them."""
+def _call(name, index, stream, args):
+    """Runs an entry point on CUDA device `index`, on `stream` or that device's current stream."""
     fn = getattr(_lib or load_library(), name)
     if stream is not None:
         if stream.device.index != index:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
-        for t in used:
-            t.record_stream(stream)
         handle = stream.cuda_stream
     elif _raw_stream is not None:
         handle = _raw_stream(index)
@@ -401,10 +415,8 @@ def mla_rope(x, positions, rope, offset=None, out=None, inverse=False, stream=No
     if shape[:lead] != at:
         raise ValueError(f"x {tuple(shape)} does not start with the shape of positions {tuple(at)}")
     index = _cuda(x)
-    used = ()
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=x.device)
-        used = (out,)
+        out = _new(shape, _BF16, x.device, stream)
     if out is x:
         o_row, o_head = x_row, x_head
     else:
@@ -413,7 +425,7 @@ def mla_rope(x, positions, rope, offset=None, out=None, inverse=False, stream=No
     width = shape[-1]
     _call("mla_rope", index, stream,
           (ctypes.byref(rope), x.data_ptr(), x_row, x_head, _data(out, index, True), o_row, o_head, rows, heads, width,
-           width - D_ROPE if offset is None else int(offset), _data(positions, index), 1 if inverse else 0), used)
+           width - D_ROPE if offset is None else int(offset), _data(positions, index), 1 if inverse else 0))
     return out
 
 
@@ -494,21 +506,16 @@ def mla_tree_decode(q, kv_cache, k_pe_cache, block_table, cache_len, W_kvb, W_o,
     pages = _pages(kv_cache, k_pe_cache, block_table.shape[1], True)
     index = _cuda(q)
     dims = make_dims(B, N, H, 0, fp8)
-    used = []
     if out is None:
-        out = torch.empty(B, N, D_MODEL, dtype=torch.bfloat16, device=q.device)
-        used.append(out)
+        out = _new((B, N, D_MODEL), torch.bfloat16, q.device, stream)
     else:
         _expect(out, "out", torch.bfloat16, (B, N, D_MODEL))
-    own_ws = workspace is None
-    ws, nbytes = _workspace(dims, MLA_ENTRY_TREE_DECODE, False, workspace, q.device)
-    if own_ws:
-        used.append(ws)
+    ws, nbytes = _workspace(dims, MLA_ENTRY_TREE_DECODE, False, workspace, q.device, stream)
     _call("mla_tree_decode", index, stream,
           (ctypes.byref(dims), ctypes.byref(pages), _data(q, index), _data(kv_cache, index), _data(k_pe_cache, index),
            _data(block_table, index), _data(cache_len, index), _data(n_nodes, index), _data(parents, index),
            _data(W_kvb, index), _data(W_kvb_scale, index), _data(W_o, index), _data(W_o_scale, index), float(scale),
-           _data(out, index), _data(ws, index), nbytes), used)
+           _data(out, index), _data(ws, index), nbytes))
     return out
 
 
