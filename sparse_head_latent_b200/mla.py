@@ -627,6 +627,12 @@ class PrefillPipeline:
         self.ws = torch.empty(max(1, mla_workspace_bytes(dims, MLA_ENTRY_PREFILL, topk is not None)),
                               dtype=torch.uint8, device=dev)
         self.h2d, self.comp, self.d2h = (torch.cuda.Stream(dev) for _ in range(3))
+        # The buffers are the current stream's: its work on what the blocks held before comes first, and they are not
+        # handed out again before the three streams are done with them.
+        for st in (self.h2d, self.comp, self.d2h):
+            st.wait_stream(torch.cuda.current_stream(dev))
+            for t in (self.ws, *(t for sl in self.slots for t in sl.values())):
+                t.record_stream(st)
         ev = lambda: [torch.cuda.Event() for _ in range(2)]  # noqa: E731
         self.ev_in, self.ev_done, self.ev_out = ev(), ev(), ev()
         self.used = [False, False]

@@ -1,4 +1,4 @@
-"""Which stream's memory a call's own tensors come from (CPU only).
+"""Which stream's memory a call's own tensors come from, and a pipeline's (CPU only).
 
 A call on `stream` writes its workspace, and a result it makes, on that stream.
 The caching allocator hands a freed block out again at once, in the order of the
@@ -107,3 +107,17 @@ def test_a_call_on_the_current_stream_needs_no_record(world, name, named):
     call(**({"stream": world.current} if named else {}))
     assert len(world.made) == makes
     assert all(t.stream is world.current and not t.users for t in world.made)
+
+
+def test_the_pipeline_orders_its_streams_with_the_memory_it_is_given(world, monkeypatch):
+    class Side(SimpleNamespace):
+        def wait_stream(self, other):
+            self.after.append(other)
+
+    streams = []
+    monkeypatch.setattr(torch.cuda, "Stream", lambda dev: streams.append(Side(after=[])) or streams[-1])
+    monkeypatch.setattr(torch.cuda, "Event", lambda: None)
+    mla.PrefillPipeline(1, 3, 2, bf(*W), bf(*O), topk=2)
+    assert len(streams) == 3 and all(s.after == [world.current] for s in streams)
+    assert len(world.made) == 11  # two slots of four inputs and a result, and the workspace
+    assert all(t.users == streams for t in world.made)
