@@ -299,10 +299,11 @@ gemm_m64_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 // grid, at most 256. One block per tile and 16 rows of it: each thread looks at
 // one CTA's share (two 64-bit divisions; one thread looking at them in turn
 // took 2 us), before the partial tiles are there, then adds two float4 columns.
+// `part` is not __restrict__: the GEMM still writes it when this kernel starts.
 constexpr int kSumRows = 16;
 constexpr int kSumThreads = 256;
 __global__ void __launch_bounds__(kSumThreads)
-sum_segments_kernel(const float* __restrict__ part, int M, int N, int K, int bm, int ctas, __nv_bfloat16* __restrict__ out) {
+sum_segments_kernel(const float* part, int M, int N, int K, int bm, int ctas, __nv_bfloat16* out) {
   __shared__ int parts[kSumThreads];
   __shared__ uint32_t found[kSumThreads / 32];
   griddep_launch();

@@ -296,7 +296,10 @@ int timed_launch(int cls, cudaStream_t stream, F&& launch) {
 // Launch of a kernel on `st`, as a dependent of the one before it if asked for
 // (see griddep_wait): then that one must call griddep_launch, the kernel must
 // call griddep_wait before it touches anything the chain's kernels write, and the
-// chain must begin with a plain launch.
+// chain must begin with a plain launch. What the chain writes changes while a
+// dependent kernel runs, so the kernel takes it without const __restrict__ and
+// reads it without __ldg: both say that it never does, and would allow the reads
+// to be moved in front of griddep_wait.
 template <class... P, class... A>
 cudaError_t launch_kernel(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
                           bool dependent, unsigned cluster, A&&... args) {
