@@ -777,7 +777,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         // Through P's shared memory, 32 of each thread's values at a time, so that
         // 64 consecutive bytes of a row leave together: stored by the threads
         // that hold them, 16 bytes a row, a tile took 8k clk.
-        float inv = l != 0.f ? 1.f / l : 0.f;
+        float inv = 1.f / l;  // l = 0: no finite score, 0 / 0
         if (p.v_scale != nullptr) inv *= __ldg(p.v_scale + (2 * (r % p.H) + 1) * 4 + (v0 >> 7));
         uint8_t* const stage = smem + S::P;
         const int who = static_cast<int>(threadIdx.x) - 64, piece = who & 15, r0 = sg.tile * kTreeRows + 64 * rank;
@@ -910,6 +910,7 @@ tree_combine_kernel(const TreeParams p, int pairs) {
   float M = -INFINITY;
 #pragma unroll 8
   for (int i = team; live && i < n; i += TEAMS) M = fmaxf(M, p.part_ml[slots[i] * kTreeRows + tr].x);
+  const float base = M == -INFINITY ? 0.f : M;
   float4 acc[QUADS];
   float sum = 0.f;
 #pragma unroll
@@ -920,7 +921,6 @@ tree_combine_kernel(const TreeParams p, int pairs) {
     float4 v[BATCH][QUADS];
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
-      ml[u].y = 0.f;
       if (i0 + u * TEAMS >= n) continue;
       const int s = slots[i0 + u * TEAMS];
       const float4* src = reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(s) * kTreeSlotFloats) +
@@ -931,8 +931,8 @@ tree_combine_kernel(const TreeParams p, int pairs) {
     }
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
-      if (ml[u].y == 0.f) continue;  // no part, or it saw none of its keys
-      const float w = ex2_approx(ml[u].x - M);
+      if (i0 + u * TEAMS >= n) continue;
+      const float w = ex2_approx(ml[u].x - base);  // 0 for a part of which the row sees no key, or none with a finite score
       sum = fmaf(w, ml[u].y, sum);
 #pragma unroll
       for (int k = 0; k < QUADS; ++k)
@@ -955,14 +955,14 @@ tree_combine_kernel(const TreeParams p, int pairs) {
     float top = M;
 #pragma unroll
     for (int i = 0; i < TEAMS - 1; ++i) top = fmaxf(top, joined[i][0][tr]);
-    const float base = top == -INFINITY ? 0.f : top, own = ex2_approx(M - base);
+    const float all = top == -INFINITY ? 0.f : top, own = ex2_approx(M - all);
     sum *= own;
 #pragma unroll
     for (int k = 0; k < QUADS; ++k) acc[k] = make_float4(acc[k].x * own, acc[k].y * own, acc[k].z * own, acc[k].w * own);
 #pragma unroll
     for (int i = 0; i < TEAMS - 1; ++i) {
       const float(*j)[kTreeRows] = joined[i];
-      const float w = ex2_approx(j[0][tr] - base);
+      const float w = ex2_approx(j[0][tr] - all);
       sum = fmaf(w, j[1][tr], sum);
 #pragma unroll
       for (int k = 0; k < QUADS; ++k)
@@ -971,7 +971,7 @@ tree_combine_kernel(const TreeParams p, int pairs) {
     }
   }
   if (!live) return;
-  float inv = sum != 0.f ? 1.f / sum : 0.f;
+  float inv = 1.f / sum;
   if (p.v_scale != nullptr) inv *= __ldg(p.v_scale + (2 * (r % p.H) + 1) * 4 + (v0 >> 7));
   uint32_t o[2 * QUADS];
 #pragma unroll
