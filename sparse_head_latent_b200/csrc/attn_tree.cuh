@@ -75,6 +75,7 @@ struct TreeParams {
   int num_pages, page_shift, table_width;
   int box_shift;                 // log2 of the keys per TMA box: min(page, 64)
   float scale_log2;              // softmax scale * log2(e)
+  const uint4* kv;               // the cache's latents again, 64 pieces a row
   const int32_t* table;          // [B][table_width]
   const int32_t* cache_len;      // [B]
   const int32_t* n_nodes;        // [B], or nullptr: N each
@@ -240,6 +241,27 @@ __device__ __forceinline__ uint32_t tree_keep(int64_t t0, int len, uint64_t sees
   if (d >= 0) return static_cast<uint32_t>(sees >> d);
   if (d <= -32) return ~0u;
   return static_cast<uint32_t>(sees << -d) | ((1u << -d) - 1u);
+}
+
+// Whether one of a sequence's positions t0 + i below `total`, i in `which`, has a
+// latent value that is not finite; `table` is the sequence's own row. For scores of
+// -inf only: out of line, one thread.
+__device__ __noinline__ bool tree_latent_not_finite(const uint4* kv, const int32_t* table, int page_shift, int num_pages,
+                                                    int64_t t0, int total, uint32_t which) {
+  for (; which != 0u; which &= which - 1u) {
+    const int64_t t = t0 + __ffs(static_cast<int>(which)) - 1;
+    if (t >= total) return false;  // rows of nodes that are not there look behind the last position
+    const int page = __ldg(table + (t >> page_shift));
+    if (page < 0 || page >= num_pages) continue;
+    const uint4* row = kv + ((static_cast<int64_t>(page) << page_shift) + (t & ((1 << page_shift) - 1))) * 64;
+    for (int i = 0; i < 64; ++i) {
+      const uint4 v = row[i];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int e = 0; e < 4; ++e)
+        if ((w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u) return true;
+    }
+  }
+  return false;
 }
 
 __global__ void __launch_bounds__(kTreeThreads, 1)
@@ -674,8 +696,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
         const bool tail = t0 + kTreeBlock > sg.len;
         if (tail) {
           const uint32_t keep = tree_keep(t0 + 64 * lh + 32 * ch, sg.len, sees);
+          uint32_t low = 0u;  // seen, with a score of -inf
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = (keep >> i) & 1 ? x[i] : -INFINITY;
+          for (int i = 0; i < 32; ++i) {
+            low |= x[i] == -INFINITY ? 1u << i : 0u;
+            x[i] = (keep >> i) & 1 ? x[i] : -INFINITY;
+          }
+          // Such a key's weight is 0, and 0 times a value that is not finite is NaN;
+          // the values no longer say so (see below), so the sum does.
+          if ((low & keep) != 0u &&
+              tree_latent_not_finite(p.kv, p.table + static_cast<int64_t>(sg.b) * p.table_width, p.page_shift, p.num_pages,
+                                     t0 + 64 * lh + 32 * ch, total, low & keep))
+            l_run = NAN;
         }
         float mx[4];
 #pragma unroll
@@ -731,7 +763,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
           // The values from the first drafted key on: those behind the last
           // position hold whatever the page held before, and 0 * NaN is
           // NaN, so they are zeroed; so is what is not finite in a drafted
-          // key's values (a row that sees it gets its NaN from the score).
+          // key's values. A row that sees such a key gets its NaN from the score,
+          // which then is not finite, or from its sum where the score is -inf.
           if (!(ok = warp_wait_all(bar(kTreeTail + (tails & 1)), (tails >> 1) & 1, ab, kErrWaitTma))) break;
           ++tails;
           {

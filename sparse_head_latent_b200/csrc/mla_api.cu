@@ -1255,6 +1255,7 @@ int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pa
   p.table_width = pg.table_width;
   p.box_shift = p.page_shift < 6 ? p.page_shift : 6;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.kv = static_cast<const uint4*>(kv);
   p.table = table;
   p.cache_len = cache_len;
   p.n_nodes = n_nodes;

@@ -50,6 +50,27 @@ def _compare(p):
     return got
 
 
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("lens,H", [([100, 126], 1), ([640, 30], 3), ([9000], 1)])
+def test_infinite_latent_of_a_drafted_key_reaches_every_node_that_sees_it(lens, H, sign, page):
+    # sign: of the key's score in head 0. -inf and +inf both have to end as NaN, in the nodes below it only.
+    p = Problem(lens, 5, H, page=page)
+    p.parents[:] = torch.tensor([-1, 0, 0, 1, 2], dtype=torch.int32)
+    clean = p.run()
+    for b in range(p.B):
+        # the largest product of both nodes that see the key, so that rounding leaves their signs; one sign for both
+        a1, a3 = _q_abs(p, b, 1)[0], _q_abs(p, b, 3)[0]
+        both = torch.where(a1 * a3 > 0, torch.minimum(a1.abs(), a3.abs()), torch.zeros_like(a1))
+        l = int(both.argmax())
+        page_, r = _at(p, b, p.lens[b] + 1)
+        p.kv[page_, r, l] = INF * sign * float(a1[l].sign())
+    got = _compare(p)
+    for j in (0, 2, 4):
+        assert torch.equal(got[:, j], clean[:, j]), j
+    assert torch.isnan(got[:, 1]).all() and torch.isnan(got[:, 3]).all()
+
+
 @pytest.mark.parametrize("lens", [[100, 126], [640, 30], [9000]])
 def test_infinite_key_with_finite_values_is_absent_where_its_score_is_lowest(lens):
     p = Problem(lens, 5, 2)
@@ -82,3 +103,14 @@ def test_infinite_latent_of_a_committed_key_in_a_share_without_finite_scores():
     l = int(a.abs().argmax())
     p.kv.view(-1, 512)[flat[700], l] = -INF * float(a[l].sign())
     assert torch.isnan(_compare(p)).all()
+
+
+def test_stale_infinities_behind_the_last_node():
+    # the table ends with the last node; rows of nodes that are not there would see positions behind it
+    p = Problem([60, 61, 10], 8, 3, page=64, nodes=[4, 3, 2], spare=0)
+    assert p.table.shape[1] == 1
+    for b in range(p.B):
+        page, r = _at(p, b, p.lens[b] + p.nodes[b] - 1)
+        p.kv[page, r + 1:], p.pe[page, r + 1:] = -INF, INF
+    p.q[..., 128] = -p.q[..., 128].abs()
+    assert not torch.isnan(_compare(p)).any()
