@@ -277,7 +277,7 @@ int mla_quantize_act(const void* x, int rows, int cols, void* codes, float* scal
 /* Rotary settings: made once per model with mla_rope_init, passed by pointer
  * (host memory, read during the call only). */
 typedef struct {
-  uint64_t turns[32];  /* per pair: angle per position / 2 pi, in units of 2^-64 */
+  uint64_t turns[32];  /* per pair: angle per position / 2 pi, in units of 2^-64, right to two of them */
   float magnitude;     /* multiplies every cosine and sine */
   int layout;          /* MLA_ROPE_INTERLEAVED or MLA_ROPE_HALF */
 } mla_rope_table;

@@ -1493,27 +1493,27 @@ int mla_rope_init(mla_rope_table* table, int layout, double base, int scaling, d
     return MLA_ERR_UNSUPPORTED;
   if (!(base > 1.0) || !std::isfinite(base) || !std::isfinite(magnitude)) return MLA_ERR_SHAPE;
   if (scaling != MLA_ROPE_UNSCALED && (!(factor >= 1.0) || !std::isfinite(factor))) return MLA_ERR_SHAPE;
-  const double pi = 3.14159265358979323846;
-  double lo = 0.0, hi = 0.0;
+  // 64-bit mantissas throughout: a double's would be 2^-54 of a frequency off, 2^8
+  // units of the table.
+  const long double two_pi = 2.0L * 3.14159265358979323846264338328L, b = base, dim = mla::kRopeDim;
+  long double lo = 0.0L, hi = 0.0L;
   if (scaling == MLA_ROPE_YARN) {
     if (!(original_len > 0.0) || !std::isfinite(original_len) || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) ||
         !std::isfinite(beta_fast))
       return MLA_ERR_SHAPE;
-    const double per = mla::kRopeDim / (2.0 * std::log(base));
-    lo = std::fmax(std::floor(per * std::log(original_len / (2.0 * pi * beta_fast))), 0.0);
-    hi = std::fmin(std::ceil(per * std::log(original_len / (2.0 * pi * beta_slow))), mla::kRopeDim - 1.0);
+    auto at = [&](double turns) { return dim * std::log(original_len / (two_pi * turns)) / (2.0L * std::log(b)); };
+    lo = std::fmax(std::floor(at(beta_fast)), 0.0L);
+    hi = std::fmin(std::ceil(at(beta_slow)), dim - 1.0L);
   }
   for (int i = 0; i < mla::kRopePairs; ++i) {
-    double f = std::pow(base, -2.0 * i / mla::kRopeDim);
+    long double f = std::pow(b, -2.0L * i / dim);
     if (scaling == MLA_ROPE_LINEAR) f /= factor;
     if (scaling == MLA_ROPE_YARN) {
-      const double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3), 0.0), 1.0);
-      f = f * (1.0 - r) + f / factor * r;
+      const long double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3L), 0.0L), 1.0L);
+      f = f * (1.0L - r) + f / factor * r;
     }
     // f <= 1 radian per position, so the fraction of a turn fits (2^64 / 2 pi < 2^62)
-    table->turns[i] = static_cast<uint64_t>(static_cast<long double>(f) / (2.0L * 3.14159265358979323846264338328L) *
-                                                18446744073709551616.0L +
-                                            0.5L);
+    table->turns[i] = static_cast<uint64_t>(f / two_pi * 18446744073709551616.0L + 0.5L);
   }
   table->magnitude = magnitude;
   table->layout = layout;

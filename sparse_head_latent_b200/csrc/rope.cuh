@@ -5,11 +5,12 @@
 //   (u, v) -> m (u cos a - v sin a, v cos a + u sin a),   a = s f_i,
 // with f_i = base^(-2i/64), scaled for long contexts when the table is made
 // (mla_rope_init). The table holds f_i / 2 pi (turns per position) as a 64-bit
-// binary fraction, so that s f_i mod one turn is one integer product with an
-// error of s 2^-65 turns: the angle of a position in the millions is as exact
-// as that of the first (a 32-bit float product is off by s 2^-25 radians,
-// 0.03 at a million). Only the leading 32 bits of the fraction then become a
-// float (error 2^-24 of half a turn).
+// binary fraction, right to two units, so that s f_i mod one turn is one integer
+// product with an error of s 2^-63 turns, 2^-32 at the farthest position: the
+// angle of a position in the millions is as exact as that of the first (a 32-bit
+// float product is off by s 2^-25 radians, 0.03 at a million). The leading 32 bits
+// of the fraction then become a float: of half a turn, 2^-31 from the table, 2^-31
+// from the bits left out and 2^-25 from the rounding are below 2^-24 together.
 //
 // Both kernels read and write every byte once and do a few operations per
 // byte, so memory bounds them; at one token it is the launch.
