@@ -370,7 +370,8 @@ int mla_cache_append(const mla_rope_table* table, const void* kv_a, long long kv
  * be in the cache already (mla_cache_append): node j of sequence b at
  * position cache_len[b] + j, whatever its depth in the tree.
  *   dims     : B sequences, T = N nodes per sequence (1 .. MLA_MAX_TREE), H,
- *              wdtype; topk and path ignored, act must be MLA_ACT_BF16
+ *              wdtype; path ignored, act must be MLA_ACT_BF16. Every position
+ *              is attended to: topk must be 0 (there is no selection to pass)
  *   q        : bf16 [B, N, H, 192], rotated
  *   block_table: int32 [B, table_width]
  *   cache_len: int32 [B], positions committed before the new ones (>= 0)
@@ -391,7 +392,7 @@ int mla_cache_append(const mla_rope_table* table, const void* kv_a, long long kv
  * bf16 copies in the workspace.
  * Workspace: mla_workspace_bytes(dims, MLA_ENTRY_TREE_DECODE, 0).
  * Errors: as for mla_decode; MLA_ERR_SHAPE also for bad pages or N, and for
- * B N H beyond 2^27. */
+ * B N H beyond 2^27; MLA_ERR_UNSUPPORTED also for topk other than 0. */
 int mla_tree_decode(const mla_dims* dims, const mla_pages* pages, const void* q, const void* kv_cache,
                     const void* k_pe_cache, const int32_t* block_table, const int32_t* cache_len,
                     const int32_t* n_nodes, const int32_t* parents, const void* W_kvb, const float* W_kvb_scale,

@@ -1355,7 +1355,7 @@ size_t mla_workspace_bytes(const mla_dims* dims, int entry, int has_topk) {
   if (check_dims(dims) != MLA_OK || entry < MLA_ENTRY_KV_UPPROJECT || entry > MLA_ENTRY_TREE_DECODE) return 0;
   if ((entry == MLA_ENTRY_DECODE || entry == MLA_ENTRY_TREE_DECODE) && dims->act != MLA_ACT_BF16) return 0;
   if (entry == MLA_ENTRY_TREE_DECODE &&
-      (dims->T > MLA_MAX_TREE || static_cast<int64_t>(dims->B) * dims->T * dims->H > kMaxQueryRows))
+      (dims->topk != 0 || dims->T > MLA_MAX_TREE || static_cast<int64_t>(dims->B) * dims->T * dims->H > kMaxQueryRows))
     return 0;
   return ws_layout(*dims, entry, has_topk != 0).total;
 }
@@ -1640,7 +1640,8 @@ int mla_tree_decode(const mla_dims* dims, const mla_pages* pages, const void* q,
       ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(cache_len) |
         reinterpret_cast<uintptr_t>(n_nodes) | reinterpret_cast<uintptr_t>(parents)) & 3u))
     return MLA_ERR_ALIGN;
-  if (dims->act != MLA_ACT_BF16) return MLA_ERR_UNSUPPORTED;
+  // A selection cannot be passed, so a model that sets one would get dense attention.
+  if (dims->act != MLA_ACT_BF16 || dims->topk != 0) return MLA_ERR_UNSUPPORTED;
   rc = begin_call(dims, MLA_ENTRY_TREE_DECODE, false, workspace, ws_bytes, &ds, &lay);
   if (rc != MLA_OK) return rc;
   return run_tree_decode(ds, *dims, *pages, lay, workspace, q, kv_cache, k_pe_cache, block_table, cache_len, n_nodes,
