@@ -542,16 +542,18 @@ def mla_cache_copy_pages(kv_cache, k_pe_cache, src, dst, stream=None):
     """Copies page src[i] onto page dst[i] in every layer. src and dst are host lists (sequences of ints or int32 CPU
     tensors) of equal length; a destination may be listed once and be no other pair's source. The caches are as for
     mla_cache_compact."""
-    n = len(src)
-    if len(dst) != n:
-        raise ValueError("src and dst must have the same length")
     lists = []
     for v in (src, dst):
         if isinstance(v, torch.Tensor):
             if v.is_cuda:
                 raise ValueError("src and dst are host lists, not CUDA tensors")
             v = v.tolist()
+        elif isinstance(v, (bytes, bytearray)):  # array takes these as raw memory, four to an index
+            raise ValueError("src and dst are sequences of ints")
         lists.append(array.array("i", v))  # OverflowError for an index beyond 32 bits
+    n = len(lists[0])  # of what the call reads
+    if len(lists[1]) != n:
+        raise ValueError("src and dst must have the same length")
     pages = _pages(kv_cache, k_pe_cache, 0, False)
     index = _cuda(kv_cache)
     _call("mla_cache_copy_pages", index, stream,

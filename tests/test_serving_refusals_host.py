@@ -1,11 +1,14 @@
 """More refusals of the paged-serving calls (CPU only; answered before the first CUDA call)."""
+import array
 import ctypes
 import random
 import time
 
 import pytest
+import torch
 
 import sparse_head_latent_b200 as mla
+from sparse_head_latent_b200 import mla as binding
 from test_serving_host import OK, SHAPE, UNSUPPORTED, WORKSPACE, _copy, _pages, _tree, lib  # noqa: F401
 
 
@@ -62,3 +65,28 @@ def test_copy_refuses_lists_that_clash(lib, n):  # noqa: F811
         assert _copy(lib, src, dst, _pages(num_pages=pool, page_size=16)) == SHAPE
     if n > 1:  # more pairs than pages have a destination twice
         assert _copy(lib, [0] * n, [0] * n, _pages(num_pages=n - 1, page_size=16)) == SHAPE
+
+
+def test_copy_reads_as_many_indexes_as_its_lists_hold(lib, monkeypatch):  # noqa: F811
+    # the addresses and the length that reach the library, with no device: a list may be any sequence of ints
+    seen = []
+
+    def call(name, index, stream, args):
+        n = args[5]
+        seen.append([list((ctypes.c_int32 * n).from_address(a)) if n else [] for a in args[3:5]])
+
+    monkeypatch.setattr(binding, "_call", call)
+    monkeypatch.setattr(binding, "_cuda", lambda t: 0)
+    monkeypatch.setattr(binding, "_data", lambda t, index: t.data_ptr())
+    kv, pe = torch.zeros(4, 16, 512, dtype=torch.bfloat16), torch.zeros(4, 16, 64, dtype=torch.bfloat16)
+    for src, dst in (([0, 1], [2, 3]), (range(2), (2, 3)), (torch.tensor([0, 1]), torch.tensor([2, 3], dtype=torch.int32)),
+                     (array.array("i", [0, 1]), array.array("q", [2, 3])), (torch.arange(4)[::2] // 2, [2, 3])):
+        mla.mla_cache_copy_pages(kv, pe, src, dst)
+        assert seen.pop() == [[0, 1], [2, 3]]
+    mla.mla_cache_copy_pages(kv, pe, [], [])
+    assert seen.pop() == [[], []]
+    for src, dst in ((bytes(8), [2, 3]), (bytes(8), bytes(8)), (bytearray(8), [1] * 8), ([0, 1], bytes(2)), ([0], [1, 2]),
+                     (bytes(4), [2])):
+        with pytest.raises(ValueError):
+            mla.mla_cache_copy_pages(kv, pe, src, dst)
+    assert not seen
