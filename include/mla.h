@@ -472,13 +472,18 @@ int mla_set_e4m3_weight_conversion(int onchip);
  * Returns MLA_ERR_CUDA if no device is usable. */
 int mla_set_wait_timeout_ns(unsigned long long ns);
 
-/* Test hook for the failure path above, off by default: while on (on != 0)
- * the producer warp of the block-dense attention kernel issues none of its
- * loads on the current device, so that the kernel's waits for them (and for
- * the tensor-core work that would follow) run into the time limit. The
- * kernel then records a 1xx code and exits cleanly; its output is
+/* Test hook for the failure path above, off (0) by default: while on, a
+ * producer warp on the current device stops issuing loads, so that its
+ * kernel's waits for them (and for the tensor-core work that would follow)
+ * run into the time limit:
+ *   1  block-dense attention: none of its loads
+ *   2  tree attention (mla_tree_decode): no keys after a tile's first block
+ *   3  few-row GEMMs (mla_decode, mla_tree_decode): no activations after a
+ *      CTA's first tile
+ * The kernel then records a 1xx code and exits cleanly; its output is
  * undefined. Nothing faults or hangs: every wait is bounded. Synchronous
- * like mla_set_wait_timeout_ns; switch it off again before normal use. */
+ * like mla_set_wait_timeout_ns; switch it off again before normal use.
+ * MLA_ERR_SHAPE for another value. */
 int mla_test_withhold_attention_loads(int on);
 
 /* Test hook, host only (no device work): the plan mla_out_project and

@@ -85,6 +85,7 @@ struct TreeParams {
   int64_t* ustart;               // [B + 2] first unit of each sequence, their number, and what a tile adds to its blocks
   float* part_o;                 // [2 pairs][128 value quads][128 rows][4] unnormalised partial tiles
   float2* part_ml;               // [2 pairs][128 rows] (max in the scaled log2 domain, sum)
+  int most_blocks;               // of a tile whose keys are loaded: all, fewer by the test hook only
   int* err;
 };
 
@@ -465,8 +466,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
           tma_load_3d_pair_warp(ring0 + ks * S::GROUP, &tm_qabs, mapa_shared(landed, rank), 0, qrow, 2 * i, issue);
           if (++ks == S::GROUPS) ks = 0, parity ^= 1;
         }
+        const int j1 = min(sg.j1, p.most_blocks);
 #pragma unroll 1
-        for (int j = sg.j0; ok && j < sg.j1; ++j, ++g) {
+        for (int j = sg.j0; ok && j < j1; ++j, ++g) {
           const int rows = row_of(j, entry);
           entry = entry_of(j + 1);
           // The rope slot: Q.K^T of the block two before has read it.
@@ -485,6 +487,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constan
             if (++ks == S::GROUPS) ks = 0, parity ^= 1;
           }
         }
+        ok = ok && j1 == sg.j1;
       }
     } else {
       const uint32_t vfull0_leader = mapa_shared(vfull0, 0), qfull_leader = mapa_shared(bar(kTreeQFull), 0);

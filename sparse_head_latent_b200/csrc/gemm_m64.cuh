@@ -65,6 +65,7 @@ struct M64Batch {
   int count;
   int a_step, b_row0, b_step;
   int c_step, ldc;
+  int most_tiles = 0x7fffffff;  // a CTA's tiles of A (and B) that are loaded; fewer by the test hook only
 };
 
 // First k-block unit of CTA c's share when `units` are cut into g shares.
@@ -181,7 +182,7 @@ gemm_m64_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const int mt = sg.mt, nt = sg.nt, sp = sg.z;
         for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
           const int s = it % S;
-          if (!mbar_wait(empty0 + 8 * s, ((it / S) & 1) ^ 1, ab, kErrWaitConsumer)) {
+          if (it >= bt.most_tiles || !mbar_wait(empty0 + 8 * s, ((it / S) & 1) ^ 1, ab, kErrWaitConsumer)) {
             ok = false;
             break;
           }

@@ -129,13 +129,13 @@ gemm_m64_w8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       const uint32_t full0 = codes ? wfull0 : afull0, empty0 = codes ? wempty0 : aempty0;
       const uint32_t base = smem_u32(smem) + (codes ? Cfg::W0 : Cfg::A0), bytes = codes ? Cfg::W_BYTES : Cfg::A_BYTES;
       const int stages = codes ? SW : SA;
-      int s = 0;
+      int s = 0, left = codes ? 0x7fffffff : bt.most_tiles;
       uint32_t parity = 1;
       bool ok = true, waited = !codes;
       while (ok && work.next(sg)) {
         const int wrow = bt.b_row0 + sg.z * bt.b_step;
         for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
-          if (!mbar_wait_short(empty0 + 8 * s, parity, ab, kErrWaitConsumer)) {
+          if (--left < 0 || !mbar_wait_short(empty0 + 8 * s, parity, ab, kErrWaitConsumer)) {
             ok = false;
             break;
           }

@@ -246,6 +246,15 @@ bool map_chunks(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_ro
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Test hook (mla_test_withhold_attention_loads): whose loads stop early.
+enum Withhold : int {
+  kWithholdNone = 0,
+  kWithholdDense = 1,    // block-dense attention: all of them (a device variable, too)
+  kWithholdTree = 2,     // tree attention: keys after a tile's first block
+  kWithholdFewRows = 3,  // few-row GEMMs: activations after a CTA's first tile
+};
+int g_withhold = kWithholdNone;
+
 // How e4m3 weights meet bf16 activations (mla_set_e4m3_weight_conversion):
 // 0 = dequantised into a bf16 workspace copy per call, 1 = converted on chip
 // by the projection GEMMs.
@@ -755,9 +764,10 @@ int launch_gemm8_wo(const DeviceState* ds, int M, int H, const void* attn8, cons
 // split of one GEMM over `grid` CTAs.
 template <class Cfg64, class Cfg128>
 int launch_m64(const DeviceState* ds, const CUtensorMap& ta, const CUtensorMap& tb, int M, int N, int K,
-               const mla::M64Batch& bt, int grid, float* part, void* out, int cls, cudaStream_t st,
+               mla::M64Batch bt, int grid, float* part, void* out, int cls, cudaStream_t st,
                bool dependent = false) {
   const int bm = M <= 64 ? 64 : 128;
+  if (g_withhold == kWithholdFewRows) bt.most_tiles = 1;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
   cudaError_t le = cudaSuccess;
   const int rc = timed_launch(cls, st, [&] {
@@ -800,8 +810,9 @@ int launch_gemm_wo_m64(const DeviceState* ds, int M, int H, const void* attn, co
 
 template <class Cfg64, class Cfg128>
 int launch_m64_w8(const DeviceState* ds, const CUtensorMap& ta, const CUtensorMap& tw, int M, int N, int K,
-                  const mla::M64Batch& bt, int grid, const float* scale, float* part, void* out, int cls, cudaStream_t st,
+                  mla::M64Batch bt, int grid, const float* scale, float* part, void* out, int cls, cudaStream_t st,
                   bool dependent) {
+  if (g_withhold == kWithholdFewRows) bt.most_tiles = 1;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
   cudaError_t le = cudaSuccess;
   const int rc = timed_launch(cls, st, [&] {
@@ -1265,6 +1276,7 @@ int launch_tree_attention(const DeviceState* ds, const mla_dims& d, const mla_pa
   p.ustart = reinterpret_cast<int64_t*>(ws_at(ws, lay.tree_start));
   p.part_o = reinterpret_cast<float*>(ws_at(ws, lay.tree_o));
   p.part_ml = reinterpret_cast<float2*>(ws_at(ws, lay.tree_ml));
+  p.most_blocks = g_withhold == kWithholdTree ? 1 : 0x7fffffff;
   p.err = ds->err;
   const uint64_t qrows = static_cast<uint64_t>(d.B) * d.T * d.H, crows = static_cast<uint64_t>(pg.num_pages) * pg.page_size;
   const uint32_t box = 1u << p.box_shift;
@@ -1803,10 +1815,13 @@ int mla_set_wait_timeout_ns(unsigned long long ns) {
 }
 
 int mla_test_withhold_attention_loads(int on) {
-  const int v = on != 0 ? 1 : 0;
+  if (on < 0 || on > kWithholdFewRows) return MLA_ERR_SHAPE;
+  const int v = on == kWithholdDense ? 1 : 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
-  return cudaMemcpyToSymbol(mla::g_mla_withhold_attn_loads, &v, sizeof v) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  if (cudaMemcpyToSymbol(mla::g_mla_withhold_attn_loads, &v, sizeof v) != cudaSuccess) return MLA_ERR_CUDA;
+  g_withhold = on;
+  return MLA_OK;
 }
 
 int mla_test_wo_split_plan(int tiles, int pairs, int num_kb, int* tail, int* split) {

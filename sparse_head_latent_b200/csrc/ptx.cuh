@@ -41,7 +41,7 @@ __device__ __forceinline__ uint64_t wait_timeout_ns() {
 // Test hook, 0 in normal use: when set, the producer of the block-dense
 // attention kernel issues none of its loads, so the kernel's bounded waits
 // expire; it exercises the abort path (error word, clean exit) without any
-// fault.
+// fault. The serving kernels take theirs as a launch parameter (Withhold).
 __device__ int g_mla_withhold_attn_loads = 0;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

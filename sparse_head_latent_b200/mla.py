@@ -582,10 +582,12 @@ def mla_set_wait_timeout_ns(ns: int):
     _check("mla_set_wait_timeout_ns", load_library().mla_set_wait_timeout_ns(int(ns)))
 
 
-def mla_test_withhold_attention_loads(on: bool):
-    """Test hook: while on, the block-dense attention kernel issues no loads
-    and its bounded waits expire (error word 1xx, clean exit)."""
-    _check("mla_test_withhold_attention_loads", load_library().mla_test_withhold_attention_loads(1 if on else 0))
+def mla_test_withhold_attention_loads(on):
+    """Test hook: while on, a kernel's producer stops issuing loads and its
+    bounded waits expire (error word 1xx, clean exit). True or 1: block-dense
+    attention; 2: tree attention, after a tile's first block; 3: few-row
+    GEMMs, after a CTA's first tile. False or 0: off."""
+    _check("mla_test_withhold_attention_loads", load_library().mla_test_withhold_attention_loads(int(on)))
 
 
 def mla_profile_begin():
