@@ -438,10 +438,19 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 }
 
 // Arrive on an mbarrier of either CTA of the pair with the default (CTA-scope
-// release) semantics. For a hand-off of tensor-memory data to the pair's
-// UMMA issuer after tcgen05.wait::st and tcgen05.fence::before_thread_sync:
-// it orders the hand-off without the cluster-scope release, which waits for
-// every outstanding memory access of the thread (about a microsecond).
+// release) semantics, without the cluster-scope release, which takes about a
+// microsecond even in a thread that has nothing else under way. It hands over to the
+// pair's UMMA issuer, and to nobody else in the other CTA, what this CTA's own
+// tensor core then reads:
+//   tensor memory, after tcgen05.wait::st and tcgen05.fence::before_thread_sync;
+//   this CTA's own shared memory, after fence.proxy.async in every lane that wrote
+//   and __syncwarp.
+// For shared memory that rests on the hardware and not on the memory model, by
+// which a CTA-scope release orders nothing for a thread of another CTA: the proxy
+// fence is done when the stores are in this SM's shared memory, the arrival
+// leaves after it, and the other CTA's issuer never reads that memory itself;
+// it only starts this SM's tensor core on it. Data that a thread of the other CTA
+// reads needs mbar_arrive_cluster.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
