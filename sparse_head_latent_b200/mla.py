@@ -399,7 +399,7 @@ def _rows_and_heads(t, shape, lead):
         elif strides[d] != row * rows:
             raise ValueError("the leading dimensions must fold into one")
         rows *= shape[d]
-    return rows, row, heads, strides[-2] if n == lead + 2 else width
+    return rows, row, heads, strides[-2] if heads > 1 else width
 
 
 def mla_rope(x, positions, rope, offset=None, out=None, inverse=False, stream=None):
