@@ -381,13 +381,23 @@ constexpr int kSplitSlots = 74;
 // 128-row UMMA tiles, one CTA per item), beyond it on the CTA-pair GEMM.
 constexpr int kFewRows = 256;
 // Trees over e4m3 codes: read as stored up to this many rows (each 128 rows
-// convert them again), through bf16 copies (95 us, once) and the CTA-pair GEMM
-// beyond. 128 heads, all products: 256 rows 128 us against 231 with copies, 512
-// rows 218 against 238, 768 rows 322 against 338; 896 would be about 360.
+// convert them again), through bf16 copies (95 us of 128 heads, once) and the
+// CTA-pair GEMM, whose last wave is not split along K here, beyond. Whole steps of 4
+// nodes over 200 positions, us, codes / copies:
+//   heads  256 rows       384            512            768            1024
+//   8      46.1 / 48.3    60.6 / 59.0    66.8 / 61.2    86.2 / 78.4    103 / 89
+//   16     52.4 / 61.2    70.8 / 74.8    79.9 / 78.0    103 / 100      125 / 110
+//   64     94.0 / 143     132 / 160      162 / 171      235 / 241      315 / 277
+//   128    157 / 254      231 / 290      304 / 321      466 / 486      595 / 537
+// One number for all of them: with 8 heads 384 would be right, and 768 costs 10 %.
 constexpr int kFewRowsE4m3 = 768;
-// Over bf16 weights: a step of 132, 192 and 256 rows took 157, 178 and 191 us on the
-// few-row kernels, launched as dependents, 158, 176 and 183 with W_o on the pair
-// GEMM, in plain launches.
+// Over bf16 weights: the few-row kernels, launched as dependents, against W_o on the
+// pair GEMM in plain launches. The same steps:
+//   heads  64 rows        128            192            256
+//   8      37.5 / 40.5    39.2 / 38.1    40.1 / 39.5    44.2 / 40.3
+//   16     40.8 / 46.9    43.8 / 45.3    47.4 / 45.5    50.0 / 47.1
+//   64     61.8 / 78.2    68.7 / 81.7    92.2 / 93.4    96.7 / 96.7
+//   128    84.4 / 121     103 / 135      155 / 153      173 / 172
 constexpr int kFewRowsTree = 192;
 constexpr int64_t tree_few_rows(bool e4m3) { return e4m3 ? kFewRowsE4m3 : kFewRowsTree; }
 // Cost model for MLA_PATH_AUTO: a tile group goes absorbed when its middle
