@@ -51,3 +51,49 @@ def test_prefill_and_decode_of_different_problems_on_two_streams():
     _in_turn([lambda d=d, **k: mla.mla_prefill(*d, w, o, **k) for d in data])
     _in_turn([lambda d=d, q=q, **k: mla.mla_decode(q, d[1], d[2], w, o, **k) for d, q in zip(data, last)])
     _in_turn([lambda d=d, **k: mla.mla_kv_upproject(d[1], w, **k) for d in data])
+
+
+def test_a_call_on_a_forked_stream_is_captured_with_the_memory_it_makes():
+    p = Problem([500, 90, 3000], 3, 16)
+    x = torch.randn(300, 16, 192, device="cuda").to(torch.bfloat16)
+    at, rope = torch.arange(300, dtype=torch.int32, device="cuda"), mla.make_rope()
+    args = dict(cache_len=p.i32(p.lens), n_nodes=p.i32(p.nodes))
+    want = p.run(**args), mla.mla_rope(x, at, rope)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        first = p.run(stream=side, **args)
+        turned = mla.mla_rope(x, at, rope, stream=side)
+        second = p.run(stream=side, **args)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for out in (first, turned, second):
+            out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, want[0]) and torch.equal(second, want[0]) and torch.equal(turned, want[1])
+    _no_device_error()
+    del graph
+
+
+def test_results_of_a_side_stream_outlive_their_names_on_the_current_one():
+    # a result dropped while the current stream still reads it is not handed to the next call on the side stream
+    side, rope = torch.cuda.Stream(), mla.make_rope()
+    at = torch.arange(4096, dtype=torch.int32, device="cuda")
+    xs = [torch.randn(4096, 32, 192, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    want = [mla.mla_rope(x, at, rope) for x in xs]
+    torch.cuda.synchronize()
+    sums = []
+    for i in range(12):
+        out = mla.mla_rope(xs[i % 2], at, rope, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        big = out
+        for _ in range(4):
+            big = big * 1  # the current stream lags behind
+        sums.append(big.clone())
+        del out, big
+    torch.cuda.synchronize()
+    for i, s in enumerate(sums):
+        assert torch.equal(s, want[i % 2])
+    _no_device_error()
