@@ -473,14 +473,14 @@ int mla_set_e4m3_weight_conversion(int onchip);
 int mla_set_wait_timeout_ns(unsigned long long ns);
 
 /* Test hook for the failure path above, off (0) by default: while on, a
- * producer warp on the current device stops issuing loads, so that its
- * kernel's waits for them (and for the tensor-core work that would follow)
- * run into the time limit:
- *   1  block-dense attention: none of its loads
+ * producer warp stops issuing loads, so that its kernel's waits for them (and
+ * for the tensor-core work that would follow) run into the time limit:
+ *   1  block-dense attention on the current device: none of its loads
  *   2  tree attention (mla_tree_decode): no keys after a tile's first block
  *   3  few-row GEMMs (mla_decode, mla_tree_decode): no activations after a
  *      CTA's first tile
- * The kernel then records a 1xx code and exits cleanly; its output is
+ * (2 and 3: calls made afterwards, on any device; a captured graph keeps what
+ * it was captured with.) The kernel then records a 1xx code and exits cleanly; its output is
  * undefined. Nothing faults or hangs: every wait is bounded. Synchronous
  * like mla_set_wait_timeout_ns; switch it off again before normal use.
  * MLA_ERR_SHAPE for another value. */

